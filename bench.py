@@ -902,6 +902,9 @@ def main():
 
 CACHE_WRITE_SOURCES = ("q8kv_cache_write.cuh", "q8kv_cache_write_api.cuh", "q8kv_ptx.cuh")
 QUEST_SOURCES = ("q8kv_quest.cuh", "q8kv_quest_api.cuh", "q8kv_ptx.cuh")
+# prefixes of the sources of kernels that no decode call launches
+OTHER_KERNELS = ("q8kv_cache_write", "q8kv_quest", "q8kv_q4", "q8kv_rope", "q8kv_mass",
+                 "q8kv_evict", "q8kv_verify")
 Q4_SOURCES = ("q8kv_q4.cuh", "q8kv_q4_api.cuh", "q8kv_ptx.cuh", "q8kv_qquant.cuh", "q8kv_decode.cuh")
 
 
@@ -922,7 +925,7 @@ def source_hash(kernel: str = "decode") -> str:
         elif kernel == "q4":
             mine = name in Q4_SOURCES
         else:
-            mine = not name.startswith(("q8kv_cache_write", "q8kv_quest", "q8kv_q4"))
+            mine = not name.startswith(OTHER_KERNELS)
         if not mine:
             continue
         with open(os.path.join(csrc, name), "rb") as f:

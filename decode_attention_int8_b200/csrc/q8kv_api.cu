@@ -401,6 +401,7 @@ struct Call {
     float scale;
     int32_t *dots;
     int dots_max_len;
+    float *lse = nullptr;                  // row statistics (q8kv_decode_attn_lse)
     int stall_cta = -1;                    // fault injection (q8kv_debug_stall_pipeline)
     unsigned long long stall_limit_ns = 0;
 };
@@ -550,6 +551,7 @@ q8kv_status run(const Call &c, void *ws, size_t ws_bytes, bool managed_ws, cudaS
     std::memset(&p, 0, sizeof(p));
     uint8_t *w = static_cast<uint8_t *>(ws);
     p.out = c.out;
+    p.lse = c.lse;
     p.q = c.q;
     p.block_table = c.bt;
     p.seq_lens = c.lens;
@@ -583,6 +585,10 @@ q8kv_status run(const Call &c, void *ws, size_t ws_bytes, bool managed_ws, cudaS
     p.heads_seg = pl.heads_seg;
     p.scratch_stride = pl.scratch_stride;
     p.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
+    // The call that also gives row statistics takes the weights' finer scale: with 24 ragged
+    // sequences of 4 query tokens the output is off by 5e-7 instead of 4e-6 (2-norm).
+    p.tc_head = c.lse ? kTcAHeadFine : kTcAHead;
+    p.tc_unit = std::ldexp(1.f, (int)p.tc_head - 22);
     p.stall_cta = c.stall_cta;
     p.stall_limit_ns = c.stall_limit_ns;
     p.lay = pl.lay;
@@ -680,6 +686,25 @@ q8kv_status q8kv_decode_attn_multi(float *out, const float *q, const int8_t *k_b
     Call c{out, q, k_blocks, v_blocks, kscale, vscale, block_table, seq_lens, sh, scale, nullptr,
            0};
     return run(c, nullptr, 0, true, stream);
+}
+
+q8kv_status q8kv_decode_attn_lse(float *out, float *lse, const float *q, const int8_t *k_blocks,
+                                 const int8_t *v_blocks, const float *kscale,
+                                 const float *vscale, const int32_t *block_table,
+                                 const int32_t *seq_lens, int B, int n_queries, int n_q_heads,
+                                 int n_kv_heads, int head_dim, int kv_block_size,
+                                 int max_blocks_per_seq, int num_kv_blocks, float scale,
+                                 void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || n_queries <= 0)
+        return Q8KV_ERR_INVALID_ARG;
+    Shape sh{B, n_q_heads, n_kv_heads, head_dim, kv_block_size, max_blocks_per_seq,
+             num_kv_blocks};
+    sh.nq = n_queries;
+    Call c{out, q, k_blocks, v_blocks, kscale, vscale, block_table, seq_lens, sh, scale, nullptr,
+           0};
+    c.lse = lse;
+    return run(c, workspace, workspace_bytes, workspace == nullptr, stream);
 }
 
 size_t q8kv_workspace_bytes(int B, int n_q_heads, int n_kv_heads, int head_dim)
@@ -874,3 +899,9 @@ int q8kv_version(void)
 
 // The q4_0-cache decode entry point.
 #include "q8kv_q4_api.cuh"
+
+// Rotary positions with the cache write, attention mass, eviction, draft verification.
+#include "q8kv_rope_api.cuh"
+#include "q8kv_verify_api.cuh"
+#include "q8kv_evict_api.cuh"
+#include "q8kv_mass_api.cuh"

@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(kCombineThreads)
             const int ti = hg / p.Gq;
             const long long orow =
                 ((long long)b * p.nq + ti) * p.Hq + (long long)kvh * p.Gq + (hg - ti * p.Gq);
+            if (p.lse && q == 0 && fl == 0)
+                p.lse[orow] = row_lse(x.m, x.s);
             float *dst = p.out + orow * 128 + q * kCombineQuarter + 4 * fl;
             *reinterpret_cast<float4 *>(dst) =
                 make_float4(x.acc.x * f, x.acc.y * f, x.acc.z * f, x.acc.w * f);

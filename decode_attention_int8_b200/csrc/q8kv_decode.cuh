@@ -152,6 +152,7 @@ constexpr uint32_t kQRowBytes = 32 * 4 + kNB * 4;
 
 struct DecodeParams {
     float *out;
+    float *lse;          // natural log of each row's sum of exp(score), [B][nq][Hq], or null
     const float *q;
     const int32_t *block_table;
     const int32_t *seq_lens;
@@ -172,6 +173,7 @@ struct DecodeParams {
     int heads_seg;       // query heads per segment (HPC * G)
     int scratch_stride;  // floats per (subtile, pair) merge region
     float scale_log2;    // softmax scale * log2(e)
+    float tc_head, tc_unit; // tensor-memory kernel: headroom h of its weights and 2^-(22 - h)
     // Pipeline fault injection (the wait time-out test; -1 = off): the producer of CTA
     // stall_cta never arrives on, nor loads into, the stage of its second tile (its first
     // when it has only one), and that CTA's waits give up after stall_limit_ns.
@@ -179,6 +181,28 @@ struct DecodeParams {
     unsigned long long stall_limit_ns;
     SmemLayout lay;
 };
+
+// Log-sum-exp (natural) of a row from its maximum M and its sum S in units of 2^M; a row that
+// saw no token has S = 0 and gets -inf.
+__device__ __forceinline__ float row_lse(float M, float S)
+{
+    return S == 0.f ? -INFINITY : (M + log2f(S)) * 0.693147180559945309f;
+}
+
+// Rows of a sequence without tokens: zero output, log-sum-exp -inf (threads t of n).
+__device__ __forceinline__ void write_empty_rows(const DecodeParams &p, int b, int t, int n)
+{
+    const int rows = p.nq * p.Hq;
+    float4 *row = reinterpret_cast<float4 *>(p.out + (long long)b * rows * kD);
+#pragma unroll 1
+    for (int i = t; i < rows * kD / 4; i += n)
+        row[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.lse) {
+#pragma unroll 1
+        for (int i = t; i < rows; i += n)
+            p.lse[(long long)b * rows + i] = -INFINITY;
+    }
+}
 
 // Wait limit of this CTA's pipeline waits.
 __device__ __forceinline__ unsigned long long wait_limit(const DecodeParams &p)
@@ -1249,6 +1273,14 @@ __device__ __forceinline__ void finalize_segment(const DecodeParams &p, WarpStat
                         store_packed(dst + g, st, pv, q, f); // ldmatrix channel order
                     }
                 }
+            if (p.lse && c == 0) {
+#pragma unroll
+                for (int r = 0; r < NT; ++r) {
+                    const int hg = slice * 16 + r * 8 + g;
+                    if ((!kPack || g < 4) && hg < p.G)
+                        p.lse[q_row(p, b, hc * p.HPC + kl, hg)] = row_lse(st.M[r], st.S[r]);
+                }
+            }
         }
         return;
     }
@@ -1571,12 +1603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("bar.arrive 3, %0;" ::"n"(kConsumerThreads + 32) : "memory");
     if (gcta == 0) { // no sequence has tokens: every row is zero
 #pragma unroll 1
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            float4 *row = reinterpret_cast<float4 *>(p.out + (long long)b * p.nq * p.Hq * kD);
-#pragma unroll 1
-            for (int i = ctid; i < p.nq * p.Hq * kD / 4; i += kConsumerThreads)
-                row[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+            write_empty_rows(p, b, ctid, kConsumerThreads);
         return;
     }
     if ((int)blockIdx.x >= gcta)
@@ -1587,10 +1615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = blockIdx.x; b < p.B; b += gcta) {
         if (prefix[b + 1] != prefix[b])
             continue;
-        float4 *row = reinterpret_cast<float4 *>(p.out + (long long)b * p.nq * p.Hq * kD);
-#pragma unroll 1
-        for (int i = ctid; i < p.nq * p.Hq * kD / 4; i += kConsumerThreads)
-            row[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        write_empty_rows(p, b, ctid, kConsumerThreads);
     }
     consumer_bar();
     consume<NT, kPack, kDump>(p, smem, prefix, t0, t1, warp, lane);

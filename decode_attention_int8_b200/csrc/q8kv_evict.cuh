@@ -1,0 +1,341 @@
+// q8kv_evict.cuh -- eviction from the q8 cache by accumulated attention weight: per (sequence,
+// KV head) keep a fixed number of tokens and move their rows, in order, to new blocks.
+//
+// What it computes, per sequence of L tokens and KV head: with L <= keep every token stays;
+// otherwise the first `sink` tokens, the last `recent` ones and, of those between, the
+// keep - sink - recent of largest mass (a NaN counts as the lowest value; equal masses go to
+// the lowest position). Kept tokens stay in order: the j-th becomes token j of the sequence's
+// new block table. Heads choose independently: attention is a sum over tokens, so head h's
+// token j and head h + 1's need not come from the same position.
+//
+// evict_select_kernel finds the set. The threshold (the last mass that stays) comes from
+// a radix selection over the order-preserving 32-bit key of the mass: three histograms (11, 11
+// and 10 bits) instead of a sort; then one pass counts, and one pass writes, the positions above
+// the threshold and the first of those equal to it. A cluster of 1 to 8 blocks takes a
+// (sequence, head); its masses are read once into shared memory (when they fit), and the
+// histograms are added up through distributed shared memory. Several copies of the histogram per
+// block keep equal digits of neighbouring tokens from serialising on one counter.
+//
+// evict_move_kernel copies: 16 bytes per lane, D / 16 lanes per row, four rows of K and of V
+// in flight per lane, heads fastest, so the rows written are contiguous for a whole token.
+// It is bound by HBM: 2 (2 D + 8) bytes per kept row. Old and new blocks do not overlap, so
+// the order of the copies does not matter.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include <cstdint>
+
+#include "q8kv_ptx.cuh"
+
+namespace q8kv {
+
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictCluster = 8;
+constexpr int kEvictBins = 2048;
+constexpr int kEvictCopies = 4; // histogram copies per block
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 4;    // rows per lane
+
+struct EvictParams {
+    const float *mass;      // [B][Hk][cap]
+    const int32_t *table, *lens, *new_table;
+    float *new_mass;        // [B][Hk][new_cap]
+    int32_t *kept;          // [B][Hk][keep]
+    int32_t *new_lens;      // [B]
+    int8_t *k, *v;
+    float *ks, *vs;
+    int B, Hk, D, bs, mbps, new_mbps, num_blocks, keep, sink, recent;
+    int cap, new_cap;       // tokens per row of mass and of new_mass
+    int in_smem;            // a block's masses fit its shared memory
+    unsigned *errors;
+};
+
+// Order-preserving key: larger masses have larger keys, -0 equals +0, NaN equals -inf.
+__device__ __forceinline__ uint32_t mass_key(float x)
+{
+    if (!(x == x))
+        x = -INFINITY;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+struct EvictShared {
+    uint32_t copies[kEvictCopies][kEvictBins];
+    uint32_t hist[2][kEvictBins]; // this block's counts, read by the cluster
+    uint32_t warp_sum[kEvictWarps];
+    uint32_t digit, rest;         // chosen digit; tokens still wanted within it
+    uint32_t gt[kEvictWarps], eq[kEvictWarps];
+    uint32_t total_gt, total_eq;  // this block's counts, read by the cluster
+};
+
+// Digit of the wanted-th largest key among the counted ones: the bin where the running count
+// from the top reaches `wanted`. Every block of the cluster computes it from all histograms.
+__device__ __forceinline__ void pick_digit(cooperative_groups::cluster_group &cluster,
+                                           EvictShared &sh, int buf, int bins, uint32_t wanted,
+                                           int tid)
+{
+    const int lane = tid & 31, warp = tid >> 5;
+    const int cs = (int)cluster.num_blocks();
+    constexpr int kPer = kEvictBins / kEvictThreads;
+    uint32_t n[kPer];
+    uint32_t sum = 0;
+    // thread t: bins bins - 1 - kPer t - i, i = 0 .. kPer - 1
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        n[i] = 0;
+    const int top = bins - 1 - kPer * tid;
+    if (top >= 0) {
+        for (int r = 0; r < cs; ++r) {
+            const uint32_t *h = cluster.map_shared_rank(&sh.hist[buf][0], r);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                n[i] += h[top - i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        sum += n[i];
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += t;
+    }
+    if (lane == 31)
+        sh.warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t run = incl - sum;
+#pragma unroll
+    for (int w = 0; w < kEvictWarps; ++w)
+        run += w < warp ? sh.warp_sum[w] : 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (run < wanted && wanted <= run + n[i]) {
+            sh.digit = (uint32_t)(top - i);
+            sh.rest = wanted - run;
+        }
+        run += n[i];
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kEvictThreads)
+    evict_select_kernel(const __grid_constant__ EvictParams p)
+{
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ __align__(16) uint8_t esm[];
+    EvictShared &sh = *reinterpret_cast<EvictShared *>(esm);
+    float *buf = reinterpret_cast<float *>(esm + sizeof(EvictShared));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int pair = blockIdx.x / cs;
+    const int b = pair / p.Hk, h = pair - b * p.Hk;
+    // the masses come from the kernel before this one on the stream
+    grid_dep_wait();
+    grid_dep_launch();
+    int L = __ldg(p.lens + b);
+    if (L < 0 || L > p.cap) {
+        if (tid == 0)
+            atomicOr(p.errors, 0x1u); // seq_len clamped
+        L = L < 0 ? 0 : p.cap;
+    }
+    const float *mass = p.mass + (long long)pair * p.cap;
+    float *new_mass = p.new_mass + (long long)pair * p.new_cap;
+    int32_t *kept = p.kept + (long long)pair * p.keep;
+    const int n_new = L < p.keep ? L : p.keep;
+    const int stride = cs * kEvictThreads, first = rank * kEvictThreads + tid;
+    if (h == 0 && rank == 0 && tid == 0)
+        p.new_lens[b] = n_new;
+    for (int j = n_new + first; j < p.new_cap; j += stride)
+        new_mass[j] = 0.f;
+    for (int j = n_new + first; j < p.keep; j += stride)
+        kept[j] = -1;
+    if (L <= p.keep) { // everything stays (all blocks of the cluster)
+        for (int j = first; j < L; j += stride) {
+            kept[j] = j;
+            new_mass[j] = mass[j];
+        }
+        return;
+    }
+
+    // this block's positions [lo, hi); the chosen ones come from [mid0, mid1)
+    const int per = ((L + cs - 1) / cs + 31) & ~31;
+    const int lo = rank * per < L ? rank * per : L;
+    const int hi = lo + per < L ? lo + per : L;
+    const int mid0 = p.sink, mid1 = L - p.recent;
+    const float *src = mass + lo; // position lo + i at src[i]
+    if (p.in_smem) {
+        for (int i = tid; i < hi - lo; i += kEvictThreads)
+            buf[i] = src[i];
+        src = buf;
+        __syncthreads();
+    }
+
+    // ---- threshold key T, and how many tokens equal to it stay
+    uint32_t T = 0xffffffffu, ties = 0;
+    uint32_t wanted = (uint32_t)(p.keep - p.sink - p.recent);
+    if (wanted > 0) { // (the same for every block)
+        uint32_t prefix = 0;
+#pragma unroll 1
+        for (int round = 0; round < 3; ++round) {
+            const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
+            const int bins = round == 2 ? 1024 : 2048;
+            const int above = shift + (round == 2 ? 10 : 11); // bits decided so far: 32 - above
+            for (int i = tid; i < kEvictCopies * kEvictBins; i += kEvictThreads)
+                (&sh.copies[0][0])[i] = 0;
+            __syncthreads();
+            uint32_t *mine = sh.copies[lane % kEvictCopies];
+            const int a = (mid0 > lo ? mid0 : lo) - lo, z = (mid1 < hi ? mid1 : hi) - lo;
+            for (int i = a + tid; i < z; i += kEvictThreads) {
+                const uint32_t key = mass_key(src[i]);
+                if (round == 0 || (key >> above) == prefix)
+                    atomicAdd(mine + ((key >> shift) & (uint32_t)(bins - 1)), 1u);
+            }
+            __syncthreads();
+            // rounds alternate two buffers: a block that counts round r + 1 has passed the
+            // barrier of round r, after which round r - 1's counts are read no more
+            for (int i = tid; i < bins; i += kEvictThreads) {
+                uint32_t s = 0;
+#pragma unroll
+                for (int c = 0; c < kEvictCopies; ++c)
+                    s += sh.copies[c][i];
+                sh.hist[round & 1][i] = s;
+            }
+            cluster.sync();
+            pick_digit(cluster, sh, round & 1, bins, wanted, tid);
+            prefix = (prefix << (round == 2 ? 10 : 11)) | sh.digit;
+            wanted = sh.rest;
+        }
+        T = prefix;
+        ties = wanted;
+    }
+
+    // ---- count, then write: warp w takes a contiguous run of positions
+    const int rows = (hi - lo + 31) >> 5;
+    const int r0 = rows * warp / kEvictWarps, r1 = rows * (warp + 1) / kEvictWarps;
+    auto classify = [&](int i, float &x, bool &gt, bool &eq) {
+        gt = eq = false;
+        x = 0.f;
+        if (i < hi - lo) {
+            const int t = lo + i;
+            x = src[i];
+            const uint32_t key = mass_key(x);
+            const bool held = t < mid0 || t >= mid1;
+            gt = held || (p.keep > p.sink + p.recent && key > T);
+            eq = !held && ties > 0 && key == T;
+        }
+    };
+    uint32_t ngt = 0, neq = 0;
+    for (int r = r0; r < r1; ++r) {
+        float x;
+        bool gt, eq;
+        classify(r * 32 + lane, x, gt, eq);
+        ngt += __popc(__ballot_sync(0xffffffffu, gt));
+        neq += __popc(__ballot_sync(0xffffffffu, eq));
+    }
+    if (lane == 0) {
+        sh.gt[warp] = ngt;
+        sh.eq[warp] = neq;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        uint32_t g = 0, e = 0;
+        for (int w = 0; w < kEvictWarps; ++w) {
+            g += sh.gt[w];
+            e += sh.eq[w];
+        }
+        sh.total_gt = g;
+        sh.total_eq = e;
+    }
+    cluster.sync();
+    uint32_t gt_before = 0, eq_before = 0;
+    for (int r = 0; r < rank; ++r) {
+        gt_before += *cluster.map_shared_rank(&sh.total_gt, r);
+        eq_before += *cluster.map_shared_rank(&sh.total_eq, r);
+    }
+    for (int w = 0; w < warp; ++w) {
+        gt_before += sh.gt[w];
+        eq_before += sh.eq[w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (int r = r0; r < r1; ++r) {
+        float x;
+        bool gt, eq;
+        classify(r * 32 + lane, x, gt, eq);
+        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+        const uint32_t e = eq_before + __popc(me & below);
+        const uint32_t pos = gt_before + __popc(mg & below) + (e < ties ? e : ties);
+        if (gt || (eq && e < ties)) {
+            kept[pos] = lo + r * 32 + lane;
+            new_mass[pos] = x;
+        }
+        gt_before += __popc(mg);
+        eq_before += __popc(me);
+    }
+    cluster.sync(); // no block leaves while its counts are read
+}
+
+// Rows of sequence blockIdx.y: row r is kept token r / Hk of head r % Hk.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const __grid_constant__ EvictParams p)
+{
+    constexpr int kLanes = D / 16; // lanes per row
+    constexpr int kPerPass = kMoveThreads / kLanes;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int b = blockIdx.y;
+    const int sub = threadIdx.x % kLanes;
+    const int rows = p.keep * p.Hk; // < 2^31 (host check)
+    const int base = blockIdx.x * kPerPass * kMoveRows + threadIdx.x / kLanes;
+    const int32_t *table = p.table + (long long)b * p.mbps;
+    const int32_t *new_table = p.new_table + (long long)b * p.new_mbps;
+    long long src[kMoveRows], dst[kMoveRows]; // row indices (slot * Hk + head), src < 0: none
+    unsigned err = 0;
+#pragma unroll
+    for (int i = 0; i < kMoveRows; ++i) {
+        src[i] = -1;
+        const int r = base + i * kPerPass;
+        if (r >= 0 && r < rows) {
+            const int j = r / p.Hk, h = r - j * p.Hk;
+            const int t = __ldcg(p.kept + ((long long)b * p.Hk + h) * p.keep + j);
+            if (t >= 0) {
+                const int from = __ldg(table + t / p.bs), to = __ldg(new_table + j / p.bs);
+                if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) {
+                    err |= 0x2u; // block-table entry outside the pool: the row is skipped
+                } else {
+                    src[i] = ((long long)from * p.bs + t % p.bs) * p.Hk + h;
+                    dst[i] = ((long long)to * p.bs + j % p.bs) * p.Hk + h;
+                    if (src[i] == dst[i])
+                        src[i] = -1; // in place already
+                }
+            }
+        }
+    }
+    uint4 k[kMoveRows], v[kMoveRows];
+    float s[kMoveRows];
+#pragma unroll
+    for (int i = 0; i < kMoveRows; ++i)
+        if (src[i] >= 0) {
+            k[i] = __ldcs(reinterpret_cast<const uint4 *>(p.k + src[i] * D) + sub);
+            v[i] = __ldcs(reinterpret_cast<const uint4 *>(p.v + src[i] * D) + sub);
+            if (sub < 2)
+                s[i] = (sub == 0 ? p.ks : p.vs)[src[i]];
+        }
+#pragma unroll
+    for (int i = 0; i < kMoveRows; ++i)
+        if (src[i] >= 0) {
+            *(reinterpret_cast<uint4 *>(p.k + dst[i] * D) + sub) = k[i];
+            *(reinterpret_cast<uint4 *>(p.v + dst[i] * D) + sub) = v[i];
+            if (sub < 2)
+                (sub == 0 ? p.ks : p.vs)[dst[i]] = s[i];
+        }
+    if (err)
+        atomicOr(p.errors, err);
+}
+
+} // namespace q8kv

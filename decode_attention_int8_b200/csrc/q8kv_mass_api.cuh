@@ -1,0 +1,106 @@
+// q8kv_mass_api.cuh -- host side of q8kv_attn_mass (include/q8kv.h): argument checks and the
+// launch of attn_mass_kernel. Included at the end of q8kv_api.cu, whose device bookkeeping
+// it uses.
+#pragma once
+
+#include "q8kv_mass.cuh"
+
+namespace {
+
+using namespace q8kv;
+
+bool g_mass_attr[kMaxDevices][3];
+
+template <int NQ>
+q8kv_status launch_mass(const MassParams &p, DeviceInfo *dev, int warps, cudaStream_t stream)
+{
+    bool &set = g_mass_attr[dev - g_dev][NQ == 4 ? 2 : NQ - 1];
+    const size_t smem = sizeof(int) * ((size_t)p.B + 1);
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (!set) {
+            Q8KV_CUDA(cudaFuncSetAttribute(attn_mass_kernel<NQ>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)(sizeof(int) * (kMassMaxBatch + 1))));
+            set = true;
+        }
+    }
+    const long long tiles = (long long)p.B * ((p.cap + kMassTile - 1) / kMassTile);
+    const long long wave = (NQ == 4 ? 2LL : 3LL) * dev->sms;
+    return launch_pdl(attn_mass_kernel<NQ>, p, (unsigned)(tiles < wave ? tiles : wave),
+                      (unsigned)warps * 32u, smem, stream);
+}
+
+} // namespace
+
+extern "C" {
+
+q8kv_status q8kv_attn_mass(float *mass, const float *q, const float *lse, const int8_t *k_blocks,
+                           const float *kscale, const int32_t *block_table,
+                           const int32_t *seq_lens, int B, int n_queries, int n_q_heads,
+                           int n_kv_heads, int head_dim, int kv_block_size,
+                           int max_blocks_per_seq, int num_kv_blocks, float scale, float decay,
+                           cudaStream_t stream)
+{
+    if (!mass || !q || !lse || !k_blocks || !kscale || !block_table || !seq_lens)
+        return Q8KV_ERR_INVALID_ARG;
+    if (B <= 0 || n_queries <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 ||
+        head_dim % 32 != 0 || kv_block_size <= 0 || max_blocks_per_seq <= 0 ||
+        num_kv_blocks <= 0 || n_q_heads % n_kv_heads != 0 || !std::isfinite(scale) ||
+        !(decay >= 0.f && decay <= 1.f))
+        return Q8KV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_blocks) ||
+        ((reinterpret_cast<uintptr_t>(mass) | reinterpret_cast<uintptr_t>(lse) |
+          reinterpret_cast<uintptr_t>(kscale) | reinterpret_cast<uintptr_t>(block_table) |
+          reinterpret_cast<uintptr_t>(seq_lens)) & 3u) != 0)
+        return Q8KV_ERR_INVALID_ARG;
+    const long long R = (long long)n_queries * (n_q_heads / n_kv_heads);
+    if (head_dim != kD || !is_pow2(kv_block_size) || kv_block_size < 16 || kv_block_size > 256 ||
+        R > 128 || B > kMassMaxBatch || n_kv_heads > 4096 ||
+        (long long)num_kv_blocks * kv_block_size >= (1LL << 31) ||
+        (long long)max_blocks_per_seq * kv_block_size >= (1LL << 30) ||
+        (long long)B * max_blocks_per_seq * (kv_block_size / 16) >= (1LL << 31))
+        return Q8KV_ERR_UNSUPPORTED;
+    DeviceInfo *dev = nullptr;
+    q8kv_status st;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        st = device_info(&dev);
+    }
+    if (st != Q8KV_OK)
+        return st;
+    MassParams p;
+    p.mass = mass;
+    p.q = q;
+    p.lse = lse;
+    p.k = k_blocks;
+    p.ks = kscale;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.B = B;
+    p.nq = n_queries;
+    p.Hq = n_q_heads;
+    p.Hk = n_kv_heads;
+    p.Gq = n_q_heads / n_kv_heads;
+    p.R = (int)R;
+    p.bs_log2 = ilog2(kv_block_size);
+    p.mbps = max_blocks_per_seq;
+    p.num_blocks = num_kv_blocks;
+    p.cap = max_blocks_per_seq * kv_block_size;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.decay = decay;
+    p.errors = dev->errors;
+    // Up to 8 warps: the heads in the fewest even passes, the tokens split over what is left.
+    const int passes = (n_kv_heads + kMassMaxWarps - 1) / kMassMaxWarps;
+    p.heads_pass = (n_kv_heads + passes - 1) / passes;
+    p.subs = kMassMaxWarps / p.heads_pass;
+    const int warps = p.heads_pass * p.subs;
+    // query rows held at once: 4, 8 or 16 per KV head (more rows take K again, from L2)
+    if (R <= 4)
+        return launch_mass<1>(p, dev, warps, stream);
+    if (R <= 8)
+        return launch_mass<2>(p, dev, warps, stream);
+    return launch_mass<4>(p, dev, warps, stream);
+}
+
+} // extern "C"

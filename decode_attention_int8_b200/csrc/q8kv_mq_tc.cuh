@@ -54,8 +54,11 @@ constexpr float kTwo23F = 8388608.0f;
 // Headroom of the weights' reference A (log2 units): a weight is w vs 2^(M - A + 22 - h), at
 // most 2^(22 - h) for the largest (score + log2 vs) seen when A was set and below 2^22
 // (< 2^23, the range of the byte planes) until a score + log2 vs exceeds A + h. A moves
-// (and the accumulated planes are folded) only then, not on every new maximum.
+// (and the accumulated planes are folded) only then, not on every new maximum. h is a launch
+// parameter (tc_head): kTcAHead, or kTcAHeadFine where three more bits of the weights count
+// for more than the folds.
 constexpr float kTcAHead = 3.f;
+constexpr float kTcAHeadFine = 0.f;
 
 // 4 consumer warpgroups (warps 0-15; warpgroup w owns rows [w R/4, (w + 1) R/4) of every
 // tile) and one of helpers: the TMA producer, the two MMA issuers, the query quantiser.
@@ -480,7 +483,7 @@ __device__ __forceinline__ float tc_row_sums(float (&v)[N], int lane)
 // PV starts from zero).
 template <int R>
 __device__ __forceinline__ void tc_fold(float (&acc)[R / kTcWGs], uint32_t tOw, float fa_lane,
-                                        bool add_o, bool rescale)
+                                        bool add_o, bool rescale, float unit)
 {
     constexpr int RH = R / kTcWGs;
     if (add_o) {
@@ -491,7 +494,7 @@ __device__ __forceinline__ void tc_fold(float (&acc)[R / kTcWGs], uint32_t tOw, 
         for (int i = 0; i < RH; ++i) {
             const float c = fmaf((float)(int)o[4 * i + 2], 65536.f,
                                  fmaf((float)(int)o[4 * i + 1], 256.f, (float)(int)o[4 * i]));
-            acc[i] = fmaf(c, 1.f / 524288.f, acc[i]); // 2^-(22 - kTcAHead)
+            acc[i] = fmaf(c, unit, acc[i]); // unit = 2^-(22 - h)
         }
     }
     if (rescale) {
@@ -668,7 +671,7 @@ __device__ void tc_consume(const DecodeParams &p, uint8_t *smem, const TcLayout 
                     const float Mn = fmaxf(Mrow, mst);
                     // the reference moves when this tile's largest score + log2 vs exceeds
                     // it by more than the headroom
-                    float An = (Arow == -INFINITY || ast > Arow + kTcAHead) ? ast : Arow;
+                    float An = (Arow == -INFINITY || ast > Arow + p.tc_head) ? ast : Arow;
                     // 2^(M - A + 19) must stay finite: with V scales more than 2^104 below
                     // the weight of the top-scoring token the reference A is raised to
                     // M - 104 (the weights of that row then keep fewer significant bits)
@@ -676,7 +679,7 @@ __device__ void tc_consume(const DecodeParams &p, uint8_t *smem, const TcLayout 
                         An = Mn - 104.f;
                     cM = Mrow == -INFINITY ? 1.f : fast_exp2(Mrow - Mn);
                     fa = Arow == -INFINITY ? 1.f : fast_exp2(Arow - An);
-                    g = An == -INFINITY ? 0.f : fast_exp2(Mn - An + (22.f - kTcAHead));
+                    g = An == -INFINITY ? 0.f : fast_exp2(Mn - An + (22.f - p.tc_head));
                     Ms = Mn == -INFINITY ? 0.f : Mn;
                     rose = An != Arow && Arow != -INFINITY;
                     Mrow = Mn;
@@ -707,7 +710,7 @@ __device__ void tc_consume(const DecodeParams &p, uint8_t *smem, const TcLayout 
                     atomicOr(p.errors, kErrTimeout);
                 } else {
                     tc_fence_after();
-                    tc_fold<R>(acc, tOw, fa, !ofresh, true);
+                    tc_fold<R>(acc, tOw, fa, !ofresh, true, p.tc_unit);
                     ofresh = true;
                     since_fold = 0;
                 }
@@ -748,7 +751,7 @@ __device__ void tc_consume(const DecodeParams &p, uint8_t *smem, const TcLayout 
                 atomicOr(p.errors, kErrTimeout);
             } else if (!ofresh) {
                 tc_fence_after();
-                tc_fold<R>(acc, tOw, 1.f, true, false);
+                tc_fold<R>(acc, tOw, 1.f, true, false, p.tc_unit);
                 tc_wait_st();
                 tc_fence_before();
             }
@@ -770,9 +773,11 @@ __device__ void tc_consume(const DecodeParams &p, uint8_t *smem, const TcLayout 
             for (int q = 0; q < 4; ++q)
                 S += lds_f32(xch + 8u * (uint32_t)(q * RH + lane));
             float f = 1.f;
-            if (complete)
+            if (complete) {
                 f = (S > 0.f && Arow != -INFINITY) ? exp2f(Arow - Mrow) / S : 0.f;
-            else if (r0 + lane < p.G)
+                if (p.lse && r0 + lane < p.G)
+                    p.lse[q_row(p, cu.b, cu.hc, r0 + lane)] = row_lse(Mrow, S);
+            } else if (r0 + lane < p.G)
                 *reinterpret_cast<float4 *>(slotp + (size_t)(r0 + lane) * kSlotRow + kD) =
                     make_float4(Mrow, S, Arow, 0.f);
             sts_f32(rowi + 16u * lane, f);
@@ -944,20 +949,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int b = blockIdx.x; b < p.B; b += gcta) {
             if (prefix[b + 1] != prefix[b])
                 continue;
-            float4 *row = reinterpret_cast<float4 *>(p.out + (long long)b * p.nq * p.Hq * kD);
-#pragma unroll 1
-            for (int i = ctid; i < p.nq * p.Hq * kD / 4; i += kTcConsumerThreads)
-                row[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            write_empty_rows(p, b, ctid, kTcConsumerThreads);
         }
         tc_consume<R>(p, smem, L, tbase, prefix, t0, t1, warp, lane);
     } else if (gcta == 0) {
 #pragma unroll 1
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            float4 *row = reinterpret_cast<float4 *>(p.out + (long long)b * p.nq * p.Hq * kD);
-#pragma unroll 1
-            for (int i = ctid; i < p.nq * p.Hq * kD / 4; i += kTcConsumerThreads)
-                row[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+            write_empty_rows(p, b, ctid, kTcConsumerThreads);
     }
     tc_fence_before();
     asm volatile("bar.arrive %0, %1;" ::"n"(kTcBarTeardown), "n"(kTcTeardownThreads)

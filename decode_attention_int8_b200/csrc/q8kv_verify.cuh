@@ -1,0 +1,354 @@
+// q8kv_verify.cuh -- verification of drafted tokens against the target's probabilities from
+// given random numbers (speculative sampling).
+//
+// What it computes, per sequence with drafts x_0 .. x_(n-1), draft probabilities q_i, target
+// probabilities p_i (i = 0 .. n) and uniforms u_i: draft i is accepted while u_i q_i(x_i) <
+// p_i(x_i). At the first refusal i the next token is drawn from the residual max(p_i - q_i, 0)
+// and, when every draft is accepted, from p_n: the smallest x whose running sum exceeds
+// u Z, Z the sum of all weights and u the sequence's last uniform.
+//
+// Products and sums are taken in fp64. The answer is a whole number: a sum over 1e5 weights in
+// fp32 is off by about 1e-7 of Z, and with that many borders in [0, Z) one draw in a few
+// hundred would name a neighbour. In fp64 the sums' order moves a border by about 1e-15 Z.
+//
+// What bounds it: HBM for large batches (one row of p, and one of q after a refusal, read
+// once), latency for small ones. A cluster of up to 8 blocks takes a sequence: every block
+// repeats the accept test (a gather of 2 n values), then sums its part of the row, each warp
+// a contiguous piece; the blocks exchange their sums through distributed shared memory (one
+// cluster barrier), and the one warp whose piece holds the border reads that piece again (from
+// L2) to find the token. One launch, no workspace.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "q8kv_ptx.cuh"
+
+namespace q8kv {
+
+constexpr unsigned kErrProbs = 0x80u; // a draft token, draft count or row of weights was unusable
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyCluster = 8;
+
+struct VerifyParams {
+    int32_t *accepted; // [B]
+    int32_t *tokens;   // [B][max_drafts + 1]
+    const void *target, *draft;
+    const int32_t *drafted, *n_drafts;
+    const float *uniforms; // [B][max_drafts + 1]
+    long long target_stride, draft_stride; // elements between rows
+    int max_drafts, vocab;
+    unsigned *errors;
+};
+
+__device__ __forceinline__ float as_f32(float x)
+{
+    return x;
+}
+__device__ __forceinline__ float as_f32(__half x)
+{
+    return __half2float(x);
+}
+__device__ __forceinline__ float as_f32(__nv_bfloat16 x)
+{
+    return __bfloat162float(x);
+}
+
+// VEC consecutive elements: one 16-byte load, or a single element.
+template <typename T, int VEC>
+struct Pack {
+    T v[VEC];
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
+{
+    Pack<T, VEC> r;
+    if constexpr (VEC == 1) {
+        r.v[0] = *p;
+    } else {
+        static_assert(VEC * sizeof(T) == 16, "one 16-byte load");
+        *reinterpret_cast<uint4 *>(r.v) = __ldg(reinterpret_cast<const uint4 *>(p));
+    }
+    return r;
+}
+
+// The weights a token is drawn from: the target's row, less the draft's (kResidual) or without
+// one token (kWithout: a draft without probabilities is certain of its token). What is not
+// above zero, NaN among it, weighs nothing.
+enum VerifyMode { kPlain = 0, kResidual = 1, kWithout = 2 };
+
+__device__ __forceinline__ double weight(int mode, float p, float q, int x, int without)
+{
+    double w = (double)p;
+    if (mode == kResidual)
+        w -= (double)q;
+    else if (mode == kWithout && x == without)
+        w = 0.0;
+    return w > 0.0 ? w : 0.0;
+}
+
+__device__ __forceinline__ double warp_sum(double x)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+__device__ __forceinline__ double warp_scan(double x, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double t = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += t;
+    }
+    return x;
+}
+
+// Sum of the weights of tokens [lo, hi), one warp (lo a multiple of VEC).
+template <typename T, int VEC>
+__device__ __forceinline__ double piece_sum(const T *pr, const T *qr, int mode, int without, int lo,
+                                            int hi, int lane)
+{
+    constexpr int U = VEC == 1 ? 8 : (VEC == 4 ? 4 : 2); // packs of each row in flight per lane
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 1
+    for (int e0 = lo + lane * VEC; e0 < hi; e0 += 32 * VEC * U) {
+        Pack<T, VEC> a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + 32 * VEC * u;
+            if (e < hi) {
+                a[u] = load_pack<T, VEC>(pr + e);
+                if (mode == kResidual)
+                    b[u] = load_pack<T, VEC>(qr + e);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + 32 * VEC * u;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (e + i < hi)
+                    acc[(u * VEC + i) & 3] +=
+                        weight(mode, as_f32(a[u].v[i]),
+                               mode == kResidual ? as_f32(b[u].v[i]) : 0.f, e + i, without);
+        }
+    }
+    return warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+}
+
+// The token of piece [lo, hi): the first whose running sum, counted from `base`, exceeds
+// `goal`, or the last of any weight when rounding leaves none. Each lane sums a contiguous
+// part; the part that crosses the goal is halved down to 32 tokens in the same way.
+template <typename T>
+__device__ int piece_find(const T *pr, const T *qr, int mode, int without, int lo, int hi,
+                          double base, double goal, int lane)
+{
+#pragma unroll 1
+    for (;;) {
+        const int part = (hi - lo + 31) / 32;
+        const int a = lo + lane * part < hi ? lo + lane * part : hi;
+        const int b = a + part < hi ? a + part : hi;
+        double s = 0.0;
+#pragma unroll 4
+        for (int e = a; e < b; ++e)
+            s += weight(mode, as_f32(pr[e]), mode == kResidual ? as_f32(qr[e]) : 0.f, e, without);
+        const double incl = base + warp_scan(s, lane);
+        unsigned at = __ballot_sync(0xffffffffu, incl > goal && s > 0.0);
+        int sel;
+        if (at) {
+            sel = __ffs(at) - 1;
+        } else { // rounding: the last part of any weight
+            at = __ballot_sync(0xffffffffu, s > 0.0);
+            sel = at ? 31 - __clz(at) : 0;
+        }
+        base = __shfl_sync(0xffffffffu, incl - s, sel);
+        lo = __shfl_sync(0xffffffffu, a, sel);
+        hi = __shfl_sync(0xffffffffu, b, sel);
+        if (part <= 1)
+            return lo;
+    }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kVerifyThreads)
+    verify_kernel(const __grid_constant__ VerifyParams p)
+{
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ double piece[kVerifyWarps]; // sums of this block's warps
+    __shared__ double total[2];            // this block's sum (read by the cluster), by attempt
+    __shared__ int first_refused, count;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const long long b = blockIdx.x / cs;
+    // the probabilities may come from the kernel before this one on the stream
+    grid_dep_wait();
+    grid_dep_launch();
+    const T *target = static_cast<const T *>(p.target) + b * (p.max_drafts + 1) * p.target_stride;
+    const T *draft = p.draft ? static_cast<const T *>(p.draft) + b * p.max_drafts * p.draft_stride
+                             : nullptr;
+    const int32_t *drafted = p.drafted + b * p.max_drafts;
+    const float *uni = p.uniforms + b * (p.max_drafts + 1);
+
+    // ---- accept test, 32 drafts at a time (every block of the cluster: no exchange needed)
+    if (warp == 0) {
+        int n = p.n_drafts ? __ldg(p.n_drafts + b) : p.max_drafts;
+        unsigned err = 0;
+        if (n < 0 || n > p.max_drafts) {
+            err |= kErrProbs;
+            n = n < 0 ? 0 : p.max_drafts;
+        }
+        int refused = n;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n && refused == n; i0 += 32) {
+            const int i = i0 + lane;
+            bool bad = false;
+            if (i < n) {
+                const int x = __ldg(drafted + i);
+                bad = true;
+                if (x >= 0 && x < p.vocab) {
+                    const double pv = (double)as_f32(target[i * p.target_stride + x]);
+                    const double qv = draft ? (double)as_f32(draft[i * p.draft_stride + x]) : 1.0;
+                    bad = !((double)__ldg(uni + i) * qv < pv);
+                } else {
+                    err |= kErrProbs;
+                }
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, bad);
+            if (m)
+                refused = i0 + __ffs(m) - 1;
+        }
+        if (err)
+            atomicOr(p.errors, err);
+        if (lane == 0) {
+            first_refused = refused;
+            count = n;
+        }
+    }
+    __syncthreads();
+    const int at = first_refused;
+    const bool refused = at < count;
+    const T *pr = target + at * p.target_stride;
+    const T *qr = refused && draft ? draft + at * p.draft_stride : pr;
+    int mode = !refused ? kPlain : (draft ? kResidual : kWithout);
+    const int without = refused ? __ldg(drafted + at) : -1;
+
+    // ---- this block's part of the row, and this warp's piece of it
+    constexpr int kUnit = 32 * VEC;
+    const int units = (p.vocab + kUnit - 1) / kUnit;
+    const int pieces = cs * kVerifyWarps;
+    const int w = rank * kVerifyWarps + warp;
+    const int u0 = (int)((long long)units * w / pieces);
+    const int u1 = (int)((long long)units * (w + 1) / pieces);
+    const int lo = u0 * kUnit < p.vocab ? u0 * kUnit : p.vocab;
+    const int hi = u1 * kUnit < p.vocab ? u1 * kUnit : p.vocab;
+
+    double Z = 0.0, before = 0.0; // all weights, those of the blocks before this one
+    int owner = 0;                // block whose part crosses the goal
+    double goal = 0.0;
+    const double u = (double)__ldg(uni + p.max_drafts);
+#pragma unroll 1
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        const double s = piece_sum<T, VEC>(pr, qr, mode, without, lo, hi, lane);
+        if (lane == 0)
+            piece[warp] = s;
+        __syncthreads();
+        double mine = 0.0;
+#pragma unroll
+        for (int i = 0; i < kVerifyWarps; ++i)
+            mine += piece[i];
+        if (tid == 0)
+            total[attempt] = mine;
+        cluster.sync();
+        double sums[kVerifyCluster];
+#pragma unroll
+        for (int r = 0; r < kVerifyCluster; ++r)
+            sums[r] = r < cs ? *cluster.map_shared_rank(&total[attempt], r) : 0.0;
+        Z = 0.0;
+#pragma unroll
+        for (int r = 0; r < kVerifyCluster; ++r)
+            Z += sums[r];
+        goal = u * Z;
+        double run = 0.0;
+        int last = 0;
+        owner = -1;
+#pragma unroll
+        for (int r = 0; r < kVerifyCluster; ++r) {
+            if (r == rank)
+                before = run;
+            run += sums[r];
+            if (sums[r] > 0.0) {
+                last = r;
+                if (owner < 0 && run > goal)
+                    owner = r;
+            }
+        }
+        if (owner < 0)
+            owner = last;
+        // a residual without weight: the refused token was as likely as the target allows, and
+        // the draw falls back to the target's own row
+        if (Z > 0.0 || mode == kPlain)
+            break;
+        mode = kPlain;
+        __syncthreads(); // piece[] is written again
+    }
+    cluster.sync(); // no block leaves while its sums are read
+
+    int32_t *tokens = p.tokens + b * (p.max_drafts + 1);
+    if (rank == 0) {
+        if (tid == 0)
+            p.accepted[b] = at;
+#pragma unroll 1
+        for (int i = tid; i <= p.max_drafts; i += kVerifyThreads)
+            if (i != at)
+                tokens[i] = i < at ? __ldg(drafted + i) : -1;
+    }
+    if (rank != owner || warp != 0)
+        return;
+    if (!(Z > 0.0 && Z < INFINITY)) { // nothing to draw from
+        if (lane == 0) {
+            tokens[at] = -1;
+            atomicOr(p.errors, kErrProbs);
+        }
+        return;
+    }
+    // the warp piece of this block that crosses the goal
+    double run = before, from = before;
+    int sel = -1, lastw = 0;
+    double lastfrom = before;
+#pragma unroll 1
+    for (int i = 0; i < kVerifyWarps; ++i) {
+        const double x = piece[i];
+        if (x > 0.0) {
+            lastw = i;
+            lastfrom = run;
+            if (sel < 0 && run + x > goal) {
+                sel = i;
+                from = run;
+            }
+        }
+        run += x;
+    }
+    if (sel < 0) {
+        sel = lastw;
+        from = lastfrom;
+    }
+    const int sw = rank * kVerifyWarps + sel;
+    const int su0 = (int)((long long)units * sw / pieces);
+    const int su1 = (int)((long long)units * (sw + 1) / pieces);
+    const int slo = su0 * kUnit < p.vocab ? su0 * kUnit : p.vocab;
+    const int shi = su1 * kUnit < p.vocab ? su1 * kUnit : p.vocab;
+    const int x = piece_find<T>(pr, qr, mode, without, slo, shi, from, goal, lane);
+    if (lane == 0)
+        tokens[at] = x;
+}
+
+} // namespace q8kv

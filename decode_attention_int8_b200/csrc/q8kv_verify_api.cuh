@@ -1,0 +1,114 @@
+// q8kv_verify_api.cuh -- host side of q8kv_verify_draft (include/q8kv.h): argument checks and
+// the launch of verify_kernel. Included at the end of q8kv_api.cu, whose device bookkeeping
+// it uses.
+#pragma once
+
+#include "q8kv_verify.cuh"
+
+namespace {
+
+using namespace q8kv;
+
+static_assert(kErrProbs == Q8KV_DEVERR_PROBS, "device error bits differ from the header");
+
+// A launch of clusters of `cs` blocks (portable sizes), programmatic dependent launch.
+template <typename Params>
+q8kv_status launch_cluster(void (*fn)(Params), const Params &p, unsigned clusters, int cs,
+                           unsigned threads, size_t smem, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(clusters * (unsigned)cs);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    Q8KV_CUDA(cudaLaunchKernelEx(&cfg, fn, p));
+    return Q8KV_OK;
+}
+
+template <typename T>
+q8kv_status launch_verify(const VerifyParams &p, int B, int sms, cudaStream_t stream)
+{
+    constexpr int kVec = 16 / (int)sizeof(T);
+    // 16-byte loads where every row starts on 16 bytes
+    const bool vec = aligned16(p.target) && p.target_stride % kVec == 0 &&
+                     (!p.draft || (aligned16(p.draft) && p.draft_stride % kVec == 0));
+    // blocks per sequence: as many as one wave holds (4 blocks of 512 threads per SM)
+    int cs = kVerifyCluster;
+    while (cs > 1 && (long long)B * cs > 4LL * sms)
+        cs /= 2;
+    return vec ? launch_cluster(verify_kernel<T, kVec>, p, (unsigned)B, cs, kVerifyThreads, 0,
+                                stream)
+               : launch_cluster(verify_kernel<T, 1>, p, (unsigned)B, cs, kVerifyThreads, 0, stream);
+}
+
+} // namespace
+
+extern "C" {
+
+q8kv_status q8kv_verify_draft(int32_t *n_accepted, int32_t *tokens, const void *target_probs,
+                              const void *draft_probs, const int32_t *draft_tokens,
+                              const int32_t *n_drafts, const float *uniforms, int B,
+                              int max_drafts, int vocab, long long target_stride,
+                              long long draft_stride, q8kv_dtype dtype, cudaStream_t stream)
+{
+    if (B < 0 || max_drafts < 0 || vocab <= 0)
+        return Q8KV_ERR_INVALID_ARG;
+    if (dtype != Q8KV_F32 && dtype != Q8KV_F16 && dtype != Q8KV_BF16)
+        return Q8KV_ERR_INVALID_ARG;
+    if (target_stride == 0)
+        target_stride = vocab;
+    if (draft_stride == 0)
+        draft_stride = vocab;
+    if (target_stride < vocab || draft_stride < vocab)
+        return Q8KV_ERR_INVALID_ARG;
+    const uintptr_t size = dtype == Q8KV_F32 ? 4 : 2;
+    if (max_drafts > 1024 || B > (1 << 24) || vocab > (1 << 30))
+        return Q8KV_ERR_UNSUPPORTED;
+    if (B == 0)
+        return Q8KV_OK;
+    if (!n_accepted || !tokens || !target_probs || !uniforms || (max_drafts > 0 && !draft_tokens))
+        return Q8KV_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(target_probs) % size) != 0 ||
+        (reinterpret_cast<uintptr_t>(draft_probs) % size) != 0 ||
+        ((reinterpret_cast<uintptr_t>(n_accepted) | reinterpret_cast<uintptr_t>(tokens) |
+          reinterpret_cast<uintptr_t>(draft_tokens) | reinterpret_cast<uintptr_t>(n_drafts) |
+          reinterpret_cast<uintptr_t>(uniforms)) & 3u) != 0)
+        return Q8KV_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    q8kv_status st;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        st = device_info(&dev);
+    }
+    if (st != Q8KV_OK)
+        return st;
+    VerifyParams p;
+    p.accepted = n_accepted;
+    p.tokens = tokens;
+    p.target = target_probs;
+    p.draft = draft_probs;
+    p.drafted = draft_tokens;
+    p.n_drafts = n_drafts;
+    p.uniforms = uniforms;
+    p.target_stride = target_stride;
+    p.draft_stride = draft_stride;
+    p.max_drafts = max_drafts;
+    p.vocab = vocab;
+    p.errors = dev->errors;
+    if (dtype == Q8KV_F32)
+        return launch_verify<float>(p, B, dev->sms, stream);
+    if (dtype == Q8KV_F16)
+        return launch_verify<__half>(p, B, dev->sms, stream);
+    return launch_verify<__nv_bfloat16>(p, B, dev->sms, stream);
+}
+
+} // extern "C"

@@ -87,6 +87,12 @@ typedef enum {
 #define Q8KV_DEVERR_NONFINITE 0x10u  /* cache write: a row held inf or NaN (codes 0, NaN scale) */
 #define Q8KV_DEVERR_META 0x20u       /* QUEST metadata: a metadata-table entry outside its pool
                                         (row skipped), or a table too short for a request */
+#define Q8KV_DEVERR_POSITION 0x40u   /* rotary write: a position outside the table (clamped)  */
+#define Q8KV_DEVERR_PROBS 0x80u      /* draft verification: a draft token or draft count out of
+                                        range, or no probability to draw a token from         */
+
+/* Element type of rows that may come in several (q8kv_rope_cache_write, q8kv_verify_draft). */
+typedef enum { Q8KV_F32 = 0, Q8KV_F16 = 1, Q8KV_BF16 = 2 } q8kv_dtype;
 
 /*
  * Decode attention with a library-managed workspace (one per device, grown on demand
@@ -334,6 +340,166 @@ q8kv_status q8kv_quest_metadata(float *maxblocks, float *minblocks, const int8_t
                                 int n_kv_heads, int head_dim, int kv_block_size,
                                 int max_blocks_per_seq, int max_meta_blocks_per_seq,
                                 int num_kv_blocks, int num_meta_blocks, cudaStream_t stream);
+
+/*
+ * Decode attention that also gives the log-sum-exp of every row: lse[b][i][h] = ln sum_t
+ * exp(s_t) over the tokens that query i of sequence b sees (-inf, with a zero output row, when
+ * it sees none), fp32 [B][n_queries][n_q_heads]. `out` is what q8kv_decode_attn_multi gives
+ * (n_queries = 1: q8kv_decode_attn), bit for bit except where that runs on tcgen05: there this
+ * call's softmax weights carry three more bits. The statistics are what q8kv_attn_mass needs,
+ * and what merges this output with attention over other tokens.
+ *   workspace  NULL: the library-managed one (same rules as q8kv_decode_attn: one per device,
+ *              not for calls that overlap). Otherwise caller-owned as in q8kv_decode_attn_ws,
+ *              of at least q8kv_workspace_bytes(B, n_queries * n_q_heads, n_kv_heads,
+ *              head_dim) bytes; calls that may overlap, two captured graphs among them, use
+ *              one each.
+ * Other arguments, shapes, errors and asynchrony as q8kv_decode_attn_multi.
+ */
+q8kv_status q8kv_decode_attn_lse(float *out, float *lse, const float *q, const int8_t *k_blocks,
+                                 const int8_t *v_blocks, const float *kscale,
+                                 const float *vscale, const int32_t *block_table,
+                                 const int32_t *seq_lens, int B, int n_queries, int n_q_heads,
+                                 int n_kv_heads, int head_dim, int kv_block_size,
+                                 int max_blocks_per_seq, int num_kv_blocks, float scale,
+                                 void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Accumulated attention weights: for every sequence b, KV head kv and token t < seq_lens[b]
+ *   mass[b][kv][t] = decay * mass[b][kv][t]
+ *                    + sum over the head's query rows (i, h) of exp(s_t - lse[b][i][h]),
+ * h over the group of kv, with the scores s_t of the decode (same int8 query, same block dots,
+ * query i seeing tokens t < seq_lens[b] - (n_queries - 1 - i)) and the statistics that
+ * q8kv_decode_attn_lse gave for the same q and cache. Summed over a sequence's tokens, one call
+ * adds n_queries * n_q_heads / n_kv_heads per KV head (less the rows that see nothing).
+ *
+ *   mass   fp32 [B][n_kv_heads][max_blocks_per_seq * kv_block_size], updated in place; entries
+ *          at or past seq_lens[b] are neither read nor written (a new token's entry starts at
+ *          whatever the caller left: zero it, or let q8kv_evict do so)
+ *   decay  in [0, 1]: 1 adds up, less forgets, 0 writes the weights without reading mass
+ *   lse    fp32 [B][n_queries][n_q_heads]
+ * Tokens of a block whose table entry is outside the pool keep their mass
+ * (Q8KV_DEVERR_BLOCK_TABLE); a seq_len out of range is clamped (Q8KV_DEVERR_SEQ_LEN). A
+ * non-finite query, scale or lse gives non-finite masses, as it gives non-finite outputs.
+ * Supported: head_dim 128; kv_block_size a power of two in [16, 256]; n_queries *
+ * n_q_heads / n_kv_heads <= 128; n_kv_heads <= 4096; B <= 16384. One kernel launch, no
+ * workspace, asynchronous on `stream`, programmatic dependent launch as the other kernels.
+ */
+q8kv_status q8kv_attn_mass(float *mass, const float *q, const float *lse, const int8_t *k_blocks,
+                           const float *kscale, const int32_t *block_table,
+                           const int32_t *seq_lens, int B, int n_queries, int n_q_heads,
+                           int n_kv_heads, int head_dim, int kv_block_size,
+                           int max_blocks_per_seq, int num_kv_blocks, float scale, float decay,
+                           cudaStream_t stream);
+
+/*
+ * Eviction by accumulated attention weight: bound every sequence to `keep` tokens per KV head
+ * and move the kept rows to new blocks. With L = seq_lens[b], and per KV head:
+ *   L <= keep: every token is kept; otherwise the first `sink` tokens, the last `recent` ones,
+ *   and the keep - sink - recent of largest mass among those between (NaN counts as the lowest
+ *   value, equal masses go to the lowest position).
+ * The kept tokens keep their order: the j-th becomes token j of the sequence under
+ * new_block_table, with its K and V codes, scales and mass. Heads choose independently (a
+ * decode sums over tokens, so token j of one head need not be token j of another). Afterwards
+ * decode with new_block_table and new_lens, and append new tokens at position new_lens[b].
+ *
+ *   k_blocks, v_blocks, kscale, vscale  the pools; rows under new_block_table are written
+ *   mass            fp32 [B][n_kv_heads][max_blocks_per_seq * kv_block_size], read
+ *   new_mass        fp32 [B][n_kv_heads][new_max_blocks_per_seq * kv_block_size], another
+ *                   buffer: the kept tokens' masses, then zeros
+ *   kept            int32 [B][n_kv_heads][keep]: old position of each kept token, then -1
+ *   new_lens        int32 [B], another buffer than seq_lens: min(seq_lens[b], keep)
+ *   new_block_table int32 [B][new_max_blocks_per_seq]; ceil(min(L, keep) / kv_block_size)
+ *                   entries are read. Its blocks must not be read by any sequence of the call
+ *                   (fresh ones from the allocator; old blocks, which other sequences may
+ *                   share, are left as they are), except that a sequence with L <= keep may
+ *                   name its own old blocks in order and then moves nothing
+ *   keep            >= 1, sink >= 0, recent >= 0, sink + recent <= keep <=
+ *                   new_max_blocks_per_seq * kv_block_size
+ * A table entry outside the pool skips the rows that need it (Q8KV_DEVERR_BLOCK_TABLE); a
+ * seq_len out of range is clamped (Q8KV_DEVERR_SEQ_LEN). Supported: head_dim 64, 128 or 256;
+ * B <= 16384; any kv_block_size; keep * n_kv_heads < 2^30. Two kernel launches, no workspace,
+ * asynchronous on `stream`, programmatic dependent launch as the other kernels.
+ */
+q8kv_status q8kv_evict(int8_t *k_blocks, int8_t *v_blocks, float *kscale, float *vscale,
+                       float *new_mass, int32_t *kept, int32_t *new_lens, const float *mass,
+                       const int32_t *block_table, const int32_t *seq_lens,
+                       const int32_t *new_block_table, int B, int n_kv_heads, int head_dim,
+                       int kv_block_size, int max_blocks_per_seq, int new_max_blocks_per_seq,
+                       int num_kv_blocks, int keep, int sink, int recent, cudaStream_t stream);
+
+/*
+ * Rotary positions with one to four axes, fused with the q8 cache write: rotate the new tokens'
+ * query and key rows, write the queries as the fp32 rows the decode reads, and quantise and
+ * store the rotated keys and the values as q8kv_cache_write does.
+ *
+ * Pair p of a rotated row (p < rotary_dim / 2) is channels (p, p + rotary_dim / 2), or (2p,
+ * 2p + 1) with `adjacent`; channels past rotary_dim pass through. With (c, s) = cos_sin[pos][p],
+ * cos_sin[pos][rotary_dim / 2 + p] at pos = positions[pair_axis[p]][i],
+ *   x1' = x1 c - x2 s,  x2' = x2 c + x1 s,
+ * products and sums rounded to fp32 one by one. Images and video give their tokens a time, a
+ * height and a width position; text gives all axes the same.
+ *
+ *   q_out          fp32 [n_tokens][n_q_heads][head_dim]; may be q_new itself (fp32 rows without
+ *                  gaps), otherwise must not overlap the inputs
+ *   q_new, k_new, v_new  rows of type dtype (16-byte aligned): (i, h) starts at element
+ *                  i * token_stride + h * head_dim
+ *   slot_mapping   int64 [n_tokens], the slot rules of q8kv_cache_write (negative: K and V of
+ *                  the token are skipped; its query is still rotated)
+ *   positions      int32 [n_axes][n_tokens]; one outside [0, max_position) is clamped and sets
+ *                  Q8KV_DEVERR_POSITION
+ *   cos_sin        fp32 [max_position][rotary_dim], 16-byte aligned: the cosines of the pairs,
+ *                  then their sines
+ *   pair_axis      host array of rotary_dim / 2 bytes, each < n_axes, read before the call
+ *                  returns; NULL: every pair on axis 0
+ *   rotary_dim     a multiple of 8, at most head_dim
+ *   q_token_stride, kv_token_stride  elements between tokens (0 = no gap; otherwise at least
+ *                  the row and a multiple of 16 bytes)
+ * n_tokens 0 enqueues nothing. Supported: head_dim 64, 128 or 256; 1 to 4 axes. One kernel
+ * launch, asynchronous on `stream`, programmatic dependent launch as q8kv_cache_write.
+ */
+q8kv_status q8kv_rope_cache_write(float *q_out, int8_t *k_blocks, int8_t *v_blocks,
+                                  float *kscale, float *vscale, const void *q_new,
+                                  const void *k_new, const void *v_new,
+                                  const int64_t *slot_mapping, const int32_t *positions,
+                                  const float *cos_sin, const uint8_t *pair_axis, int n_tokens,
+                                  int n_axes, int n_q_heads, int n_kv_heads, int head_dim,
+                                  int rotary_dim, int adjacent, int max_position,
+                                  q8kv_dtype dtype, int kv_block_size, int num_kv_blocks,
+                                  long long q_token_stride, long long kv_token_stride,
+                                  cudaStream_t stream);
+
+/*
+ * Verification of drafted tokens (speculative sampling) against the target's probabilities,
+ * from given random numbers: the step after q8kv_decode_attn_multi scored the drafts. Sequence
+ * b with n = n_drafts[b] drafts x_0 .. x_(n-1) accepts draft i while
+ *   uniforms[b][i] * draft_probs[b][i][x_i] < target_probs[b][i][x_i].
+ * At the first refusal i it draws from max(target_probs[b][i] - draft_probs[b][i], 0), or from
+ * target_probs[b][i] when that is zero everywhere; with every draft accepted, from
+ * target_probs[b][n]. The draw is the smallest token whose running sum of weights (lowest token
+ * first) exceeds uniforms[b][max_drafts] times their total. Products and sums are fp64. Rows
+ * need not sum to one; a weight that is not above zero (NaN too) counts as zero.
+ *
+ *   n_accepted    int32 [B]
+ *   tokens        int32 [B][max_drafts + 1]: the accepted drafts, the drawn token, then -1
+ *   target_probs  dtype [B][max_drafts + 1] rows of vocab, target_stride elements apart
+ *   draft_probs   dtype [B][max_drafts] rows, draft_stride elements apart; NULL for drafts
+ *                 without probabilities (each is then certain: accepted while uniform <
+ *                 target's, and a refusal draws from the target's row without the token)
+ *   draft_tokens  int32 [B][max_drafts] (may be NULL when max_drafts is 0)
+ *   n_drafts      int32 [B], or NULL: max_drafts each
+ *   uniforms      fp32 [B][max_drafts + 1], in [0, 1)
+ *   strides       0 = vocab; otherwise at least vocab (rows that start on 16 bytes are read
+ *                 with 16-byte loads)
+ * A draft count out of range is clamped, a draft token outside the vocabulary is refused, and a
+ * row without a positive finite total gives token -1; each sets Q8KV_DEVERR_PROBS. B = 0 enqueues
+ * nothing. Supported: max_drafts <= 1024, vocab <= 2^30, B <= 2^24. One kernel launch (clusters of
+ * up to 8 blocks), no workspace, asynchronous on `stream`, programmatic dependent launch.
+ */
+q8kv_status q8kv_verify_draft(int32_t *n_accepted, int32_t *tokens, const void *target_probs,
+                              const void *draft_probs, const int32_t *draft_tokens,
+                              const int32_t *n_drafts, const float *uniforms, int B,
+                              int max_drafts, int vocab, long long target_stride,
+                              long long draft_stride, q8kv_dtype dtype, cudaStream_t stream);
 
 /* Debug: the Q quantisation alone (step 1) on n_rows rows of head_dim fp32 values
  * (head_dim a multiple of 32). qi int8 [n_rows][head_dim], qsc fp32
