@@ -341,23 +341,44 @@ def q8kv_quest_metadata(maxblocks, minblocks, k_blocks, kscale, block_table, seq
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # q8kv_dtype
 
 
-def _on_device(tensors):
-    """The device all of ``tensors`` (None among them allowed) lie on; a launch goes there
-    whatever device is current."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    return dev
+def _addr(t, name, dtype, shape, device):
+    """Data pointer of a contiguous tensor of this type and shape on CUDA device `device` (an
+    index). One round of checks per tensor: a small call's time is the host's."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on "
+                         f"cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _launch(name, dev, stream, *args):
-    """Call the entry point ``name`` with the arguments and the stream on device ``dev``."""
-    if dev.index == torch.cuda.current_device():
-        _check(getattr(lib(), name)(*args, _stream(stream)), name)
+def _cuda_index(t, name, ndim):
+    """Device index of the tensor that gives a call its sizes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dim() != ndim:
+        raise ValueError(f"{name}: expected a CUDA tensor with {ndim} dims, got "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.get_device()
+
+
+def _launch(name, device, stream, *args):
+    """Call the entry point `name` on CUDA device `device`, whichever is current: `args`, then
+    the stream (the device's current one by default)."""
+    fn = getattr(_lib or lib(), name)
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream))
+    elif stream is None:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
-        with torch.cuda.device(dev):
-            _check(getattr(lib(), name)(*args, _stream(stream)), name)
+        status = fn(*args, _stream(stream))
+    if status:
+        raise Q8KVError(status, name)
+
+
+_F32, _I32, _I64, _I8 = torch.float32, torch.int32, torch.int64, torch.int8
 
 
 def q8kv_decode_attn_lse(out, lse, q, k_blocks, v_blocks, kscale, vscale, block_table, seq_lens,
@@ -366,23 +387,26 @@ def q8kv_decode_attn_lse(out, lse, q, k_blocks, v_blocks, kscale, vscale, block_
     every row to lse [B][n_queries][Hq] (-inf for a row that sees no token). ``workspace``: a
     CUDA tensor of q8kv_workspace_bytes(B, n_queries * Hq, Hk, D) bytes, or None for the
     library-managed one."""
-    _need(out, "out", torch.float32, 4)
-    _need(q, "q", torch.float32, 4)
-    _need(lse, "lse", torch.float32, 3)
-    if tuple(out.shape) != tuple(q.shape) or tuple(lse.shape) != tuple(q.shape[:3]):
-        raise ValueError("out must have the shape of q [B][n_queries][Hq][D], and lse "
-                         "[B][n_queries][Hq]")
+    dev = _cuda_index(q, "q", 4)
+    _cuda_index(k_blocks, "k_blocks", 4)
+    _cuda_index(block_table, "block_table", 2)
     B, nq, Hq, D = q.shape
-    geo = _geometry(out[:, 0], q[:, 0], k_blocks, v_blocks, kscale, vscale, block_table,
-                    seq_lens, contiguous=False)
-    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    dev = _on_device((out, lse, q, k_blocks, v_blocks, kscale, vscale, block_table, seq_lens,
-                      workspace))
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch("q8kv_decode_attn_lse", dev, stream, _ptr(out), _ptr(lse), _ptr(q), _ptr(k_blocks),
-            _ptr(v_blocks), _ptr(kscale), _ptr(vscale), _ptr(block_table), _ptr(seq_lens),
-            geo[0], nq, *geo[1:], float(scale), _ptr(workspace), nbytes)
+    P, bs, Hk, _ = pool = k_blocks.shape
+    mbps = block_table.shape[1]
+    wptr, nbytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+        wptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch("q8kv_decode_attn_lse", dev, stream, _addr(out, "out", _F32, q.shape, dev),
+            _addr(lse, "lse", _F32, (B, nq, Hq), dev), _addr(q, "q", _F32, q.shape, dev),
+            _addr(k_blocks, "k_blocks", _I8, (P, bs, Hk, D), dev),
+            _addr(v_blocks, "v_blocks", _I8, pool, dev),
+            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
+            _addr(vscale, "vscale", _F32, (P, bs, Hk), dev),
+            _addr(block_table, "block_table", _I32, (B, mbps), dev),
+            _addr(seq_lens, "seq_lens", _I32, (B,), dev), B, nq, Hq, Hk, D, bs, mbps, P, scale,
+            wptr, nbytes)
     return out
 
 
@@ -391,26 +415,19 @@ def q8kv_attn_mass(mass, q, lse, k_blocks, kscale, block_table, seq_lens, scale,
     """mass[b][kv][t] = decay * mass[b][kv][t] + sum over the head's query rows of
     exp(score - lse): mass fp32 [B][Hk][max_blocks * block_size], q [B][n_queries][Hq][D], lse
     [B][n_queries][Hq] as q8kv_decode_attn_lse left it."""
-    _need(mass, "mass", torch.float32, 3)
-    _need(q, "q", torch.float32, 4)
-    _need(lse, "lse", torch.float32, 3)
-    _need(k_blocks, "k_blocks", torch.int8, 4)
-    _need(kscale, "kscale", torch.float32, 3)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
+    dev = _cuda_index(q, "q", 4)
+    _cuda_index(k_blocks, "k_blocks", 4)
+    _cuda_index(block_table, "block_table", 2)
     B, nq, Hq, D = q.shape
-    P, bs, Hk, Dk = k_blocks.shape
+    P, bs, Hk, _ = k_blocks.shape
     mbps = block_table.shape[1]
-    if tuple(lse.shape) != (B, nq, Hq) or Dk != D or tuple(kscale.shape) != (P, bs, Hk):
-        raise ValueError("q/lse/k_blocks/kscale shapes disagree")
-    if block_table.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("block_table/seq_lens batch dimension disagrees with q")
-    if tuple(mass.shape) != (B, Hk, mbps * bs):
-        raise ValueError(f"mass must be {(B, Hk, mbps * bs)}, got {tuple(mass.shape)}")
-    dev = _on_device((mass, q, lse, k_blocks, kscale, block_table, seq_lens))
-    _launch("q8kv_attn_mass", dev, stream, _ptr(mass), _ptr(q), _ptr(lse), _ptr(k_blocks),
-            _ptr(kscale), _ptr(block_table), _ptr(seq_lens), B, nq, Hq, Hk, D, bs, mbps, P,
-            float(scale), float(decay))
+    _launch("q8kv_attn_mass", dev, stream, _addr(mass, "mass", _F32, (B, Hk, mbps * bs), dev),
+            _addr(q, "q", _F32, q.shape, dev), _addr(lse, "lse", _F32, (B, nq, Hq), dev),
+            _addr(k_blocks, "k_blocks", _I8, (P, bs, Hk, D), dev),
+            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
+            _addr(block_table, "block_table", _I32, (B, mbps), dev),
+            _addr(seq_lens, "seq_lens", _I32, (B,), dev), B, nq, Hq, Hk, D, bs, mbps, P, scale,
+            decay)
     return mass
 
 
@@ -420,45 +437,40 @@ def q8kv_evict(k_blocks, v_blocks, kscale, vscale, new_mass, kept, new_lens, mas
     ``recent``, the heaviest others -- and move their rows, in order, to the blocks of
     new_block_table. Writes new_mass fp32 [B][Hk][new_max_blocks * block_size], kept int32
     [B][Hk][keep] (old positions, then -1) and new_lens int32 [B]."""
-    _need(k_blocks, "k_blocks", torch.int8, 4)
-    _need(v_blocks, "v_blocks", torch.int8, 4)
-    _need(kscale, "kscale", torch.float32, 3)
-    _need(vscale, "vscale", torch.float32, 3)
-    _need(new_mass, "new_mass", torch.float32, 3)
-    _need(kept, "kept", torch.int32, 3)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    _need(mass, "mass", torch.float32, 3)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(new_block_table, "new_block_table", torch.int32, 2)
-    P, bs, Hk, D = k_blocks.shape
+    dev = _cuda_index(k_blocks, "k_blocks", 4)
+    _cuda_index(kept, "kept", 3)
+    _cuda_index(block_table, "block_table", 2)
+    _cuda_index(new_block_table, "new_block_table", 2)
+    P, bs, Hk, D = pool = k_blocks.shape
     B, mbps = block_table.shape
     new_mbps, keep = new_block_table.shape[1], kept.shape[2]
-    if tuple(v_blocks.shape) != (P, bs, Hk, D) or tuple(kscale.shape) != (P, bs, Hk) or \
-            tuple(vscale.shape) != (P, bs, Hk):
-        raise ValueError("pool shapes disagree")
-    if tuple(mass.shape) != (B, Hk, mbps * bs) or tuple(new_mass.shape) != (B, Hk, new_mbps * bs):
-        raise ValueError("mass and new_mass must be [B][Hk][max_blocks * block_size] of their "
-                         "block tables")
-    if tuple(kept.shape[:2]) != (B, Hk) or seq_lens.shape[0] != B or new_lens.shape[0] != B or \
-            new_block_table.shape[0] != B:
-        raise ValueError("batch or head dimensions disagree")
-    dev = _on_device((k_blocks, v_blocks, kscale, vscale, new_mass, kept, new_lens, mass,
-                      block_table, seq_lens, new_block_table))
-    _launch("q8kv_evict", dev, stream, _ptr(k_blocks), _ptr(v_blocks), _ptr(kscale), _ptr(vscale),
-            _ptr(new_mass), _ptr(kept), _ptr(new_lens), _ptr(mass), _ptr(block_table),
-            _ptr(seq_lens), _ptr(new_block_table), B, Hk, D, bs, mbps, new_mbps, P, keep,
-            int(sink), int(recent))
+    _launch("q8kv_evict", dev, stream, _addr(k_blocks, "k_blocks", _I8, pool, dev),
+            _addr(v_blocks, "v_blocks", _I8, pool, dev),
+            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
+            _addr(vscale, "vscale", _F32, (P, bs, Hk), dev),
+            _addr(new_mass, "new_mass", _F32, (B, Hk, new_mbps * bs), dev),
+            _addr(kept, "kept", _I32, (B, Hk, keep), dev),
+            _addr(new_lens, "new_lens", _I32, (B,), dev),
+            _addr(mass, "mass", _F32, (B, Hk, mbps * bs), dev),
+            _addr(block_table, "block_table", _I32, (B, mbps), dev),
+            _addr(seq_lens, "seq_lens", _I32, (B,), dev),
+            _addr(new_block_table, "new_block_table", _I32, (B, new_mbps), dev), B, Hk, D, bs,
+            mbps, new_mbps, P, keep, sink, recent)
 
 
-def _row_stride(t, name, shape, dtype):
-    """Token stride of rows [n][heads][D] whose last two dimensions have no gaps."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA {dtype} tensor")
-    if tuple(t.shape) != shape or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
-        raise ValueError(f"{name}: expected shape {shape} with contiguous rows, got "
-                         f"{tuple(t.shape)} strides {t.stride()}")
-    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+def _token_rows(t, name, dtype, shape, device):
+    """(data pointer, token stride) of rows [n][heads][D] whose last two dimensions have no
+    gaps."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    n, heads, D = shape
+    strides = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or strides[2] != 1 or \
+            (heads > 1 and strides[1] != D):
+        raise ValueError(f"{name}: expected a {dtype} tensor {tuple(shape)} on cuda:{device} "
+                         f"with contiguous rows, got {t.dtype} {tuple(t.shape)} on {t.device} "
+                         f"with strides {strides}")
+    return t.data_ptr(), strides[0] if n > 1 else heads * D
 
 
 def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_new, v_new,
@@ -468,30 +480,23 @@ def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_ne
     and v_new to the q8 cache at slot_mapping (int64 [n], negative = padding). q_new, k_new
     and v_new: one of float32, float16, bfloat16, token dimension strided (k_new and v_new
     alike). positions int32 [n_axes][n]; cos_sin fp32 [max_position][rotary_dim], cosines then
-    sines; pair_axis: the axis of each of the rotary_dim / 2 pairs (a host sequence), None for
-    one axis; adjacent: pairs (2p, 2p + 1) instead of (p, p + rotary_dim / 2)."""
-    _need(q_out, "q_out", torch.float32, 3)
-    _need(k_blocks, "k_blocks", torch.int8, 4)
-    _need(v_blocks, "v_blocks", torch.int8, 4)
-    _need(kscale, "kscale", torch.float32, 3)
-    _need(vscale, "vscale", torch.float32, 3)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    _need(positions, "positions", torch.int32, 2)
-    _need(cos_sin, "cos_sin", torch.float32, 2)
-    P, bs, Hk, D = k_blocks.shape
-    if tuple(v_blocks.shape) != (P, bs, Hk, D) or tuple(kscale.shape) != (P, bs, Hk) or \
-            tuple(vscale.shape) != (P, bs, Hk):
-        raise ValueError("pool shapes disagree")
-    n, Hq, Dq = q_out.shape
+    sines; pair_axis: the axis of each of the rotary_dim / 2 pairs (a host sequence or bytes),
+    None for one axis; adjacent: pairs (2p, 2p + 1) instead of (p, p + rotary_dim / 2)."""
+    dev = _cuda_index(q_out, "q_out", 3)
+    _cuda_index(k_blocks, "k_blocks", 4)
+    _cuda_index(positions, "positions", 2)
+    _cuda_index(cos_sin, "cos_sin", 2)
+    P, bs, Hk, D = pool = k_blocks.shape
+    n, Hq, _ = q_out.shape
     axes = positions.shape[0]
-    if Dq != D or slot_mapping.shape[0] != n or positions.shape[1] != n:
-        raise ValueError("q_out, slot_mapping, positions and the pools disagree")
     dtype = q_new.dtype
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError(f"q_new: expected float32, float16 or bfloat16, got {dtype}")
-    q_stride = _row_stride(q_new, "q_new", (n, Hq, D), dtype)
-    kv_stride = _row_stride(k_new, "k_new", (n, Hk, D), dtype)
-    if _row_stride(v_new, "v_new", (n, Hk, D), dtype) != kv_stride:
+    qp, q_stride = _token_rows(q_new, "q_new", dtype, (n, Hq, D), dev)
+    kp, kv_stride = _token_rows(k_new, "k_new", dtype, (n, Hk, D), dev)
+    vp, v_stride = _token_rows(v_new, "v_new", dtype, (n, Hk, D), dev)
+    if v_stride != kv_stride:
         raise ValueError("k_new and v_new must have the same token stride")
     max_position, rot = cos_sin.shape
     axis = None
@@ -499,25 +504,33 @@ def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_ne
         axis = bytes(pair_axis)
         if len(axis) != rot // 2:
             raise ValueError(f"pair_axis needs {rot // 2} entries, got {len(axis)}")
-    dev = _on_device((q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_new, v_new,
-                      slot_mapping, positions, cos_sin))
-    _launch("q8kv_rope_cache_write", dev, stream, _ptr(q_out), _ptr(k_blocks), _ptr(v_blocks),
-            _ptr(kscale), _ptr(vscale), _ptr(q_new), _ptr(k_new), _ptr(v_new),
-            _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), axis, n, axes, Hq, Hk, D, rot,
-            1 if adjacent else 0, max_position, _DTYPES[dtype], bs, P, q_stride, kv_stride)
+    _launch("q8kv_rope_cache_write", dev, stream, _addr(q_out, "q_out", _F32, (n, Hq, D), dev),
+            _addr(k_blocks, "k_blocks", _I8, pool, dev),
+            _addr(v_blocks, "v_blocks", _I8, pool, dev),
+            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
+            _addr(vscale, "vscale", _F32, (P, bs, Hk), dev), qp, kp, vp,
+            _addr(slot_mapping, "slot_mapping", _I64, (n,), dev),
+            _addr(positions, "positions", _I32, (axes, n), dev),
+            _addr(cos_sin, "cos_sin", _F32, (max_position, rot), dev), axis, n, axes, Hq, Hk, D,
+            rot, 1 if adjacent else 0, max_position, code, bs, P, q_stride, kv_stride)
     return q_out
 
 
-def _prob_stride(t, name, shape):
-    """Elements between consecutive rows of probabilities [B][rows][vocab]."""
-    if tuple(t.shape) != shape or not t.is_cuda or (shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name}: expected a CUDA tensor {shape} with contiguous rows, got "
-                         f"{tuple(t.shape)} strides {t.stride()}")
+def _prob_rows(t, name, dtype, shape, device):
+    """(data pointer, elements between rows) of probabilities [B][rows][vocab]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     B, rows, vocab = shape
-    stride = t.stride(1) if rows > 1 else (t.stride(0) if B > 1 else vocab)
-    if rows > 1 and B > 1 and t.stride(0) != rows * stride:
-        raise ValueError(f"{name}: rows of consecutive sequences must be evenly spaced")
-    return stride
+    strides = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or \
+            (vocab > 1 and strides[2] != 1):
+        raise ValueError(f"{name}: expected a {dtype} tensor {tuple(shape)} on cuda:{device} "
+                         f"with contiguous rows, got {t.dtype} {tuple(t.shape)} on {t.device} "
+                         f"with strides {strides}")
+    stride = strides[1] if rows > 1 else (strides[0] if B > 1 else vocab)
+    if rows > 1 and B > 1 and strides[0] != rows * stride:
+        raise ValueError(f"{name}: the rows of consecutive sequences must be evenly spaced")
+    return t.data_ptr(), stride
 
 
 def q8kv_verify_draft(n_accepted, tokens, target_probs, draft_probs, draft_tokens, uniforms,
@@ -527,33 +540,23 @@ def q8kv_verify_draft(n_accepted, tokens, target_probs, draft_probs, draft_token
     probabilities), draft_tokens int32 [B][n], uniforms fp32 [B][n + 1] (the last one draws),
     n_drafts int32 [B] or None. Writes n_accepted int32 [B] and tokens int32 [B][n + 1]: the
     accepted drafts, the drawn token, then -1."""
-    _need(n_accepted, "n_accepted", torch.int32, 1)
-    _need(tokens, "tokens", torch.int32, 2)
-    _need(draft_tokens, "draft_tokens", torch.int32, 2)
-    _need(uniforms, "uniforms", torch.float32, 2)
-    B, n1 = tokens.shape
+    dev = _cuda_index(target_probs, "target_probs", 3)
+    B, n1, vocab = target_probs.shape
     n = n1 - 1
-    dtype, vocab = target_probs.dtype, target_probs.shape[-1]
-    if dtype not in _DTYPES:
+    dtype = target_probs.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError(f"target_probs: expected float32, float16 or bfloat16, got {dtype}")
-    if n_accepted.shape[0] != B or tuple(draft_tokens.shape) != (B, n) or \
-            tuple(uniforms.shape) != (B, n1):
-        raise ValueError("n_accepted, tokens, draft_tokens and uniforms disagree")
-    ts = _prob_stride(target_probs, "target_probs", (B, n1, vocab))
-    ds = 0
-    if draft_probs is not None:
-        if draft_probs.dtype != dtype:
-            raise ValueError("draft_probs must have the type of target_probs")
-        ds = _prob_stride(draft_probs, "draft_probs", (B, n, vocab)) if n else 0
-    if n_drafts is not None:
-        _need(n_drafts, "n_drafts", torch.int32, 1)
-        if n_drafts.shape[0] != B:
-            raise ValueError("n_drafts must have one entry per sequence")
-    dev = _on_device((n_accepted, tokens, target_probs, draft_probs, draft_tokens, uniforms,
-                      n_drafts))
-    _launch("q8kv_verify_draft", dev, stream, _ptr(n_accepted), _ptr(tokens), _ptr(target_probs),
-            _ptr(draft_probs) if n else None, _ptr(draft_tokens), _ptr(n_drafts), _ptr(uniforms),
-            B, n, vocab, ts, ds, _DTYPES[dtype])
+    tp, ts = _prob_rows(target_probs, "target_probs", dtype, (B, n1, vocab), dev)
+    dp, ds = None, 0
+    if draft_probs is not None and n:
+        dp, ds = _prob_rows(draft_probs, "draft_probs", dtype, (B, n, vocab), dev)
+    _launch("q8kv_verify_draft", dev, stream,
+            _addr(n_accepted, "n_accepted", _I32, (B,), dev),
+            _addr(tokens, "tokens", _I32, (B, n1), dev), tp, dp,
+            _addr(draft_tokens, "draft_tokens", _I32, (B, n), dev),
+            None if n_drafts is None else _addr(n_drafts, "n_drafts", _I32, (B,), dev),
+            _addr(uniforms, "uniforms", _F32, (B, n1), dev), B, n, vocab, ts, ds, code)
     return tokens
 
 

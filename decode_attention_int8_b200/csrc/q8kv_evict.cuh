@@ -11,15 +11,18 @@
 // evict_select_kernel finds the set. The threshold (the last mass that stays) comes from
 // a radix selection over the order-preserving 32-bit key of the mass: three histograms (11, 11
 // and 10 bits) instead of a sort; then one pass counts, and one pass writes, the positions above
-// the threshold and the first of those equal to it. A cluster of 1 to 8 blocks takes a
-// (sequence, head); its masses are read once into shared memory (when they fit), and the
-// histograms are added up through distributed shared memory. Several copies of the histogram per
-// block keep equal digits of neighbouring tokens from serialising on one counter.
+// the threshold and the first of those equal to it. A block takes a (sequence, head), or a
+// cluster of up to 8 when there are few of them or their masses do not fit one block's shared
+// memory: the masses are read once, and the blocks' histograms are added up through distributed
+// shared memory. Its time is latency (barriers and dependent steps), so loads go 16 at a time and
+// blocks are as large as they get. Several copies of the histogram per block keep equal digits
+// of neighbouring tokens from serialising on one counter.
 //
-// evict_move_kernel copies: 16 bytes per lane, D / 16 lanes per row, four rows of K and of V
-// in flight per lane, heads fastest, so the rows written are contiguous for a whole token.
-// It is bound by HBM: 2 (2 D + 8) bytes per kept row. Old and new blocks do not overlap, so
-// the order of the copies does not matter.
+// evict_move_kernel copies. A warp takes 32 rows: each lane looks up one row's place (position,
+// two table entries) and moves its scales, then the warp moves the rows, D / 16 lanes of 16 bytes
+// a row, the places passed on by shuffles. Heads run fastest, so the rows written are contiguous
+// for a whole token. It is bound by HBM: 2 (2 D + 8) bytes per kept row. Old and new blocks do
+// not overlap, so the order of the copies does not matter.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -30,13 +33,14 @@
 
 namespace q8kv {
 
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
+static_assert(kEvictWarps == 32, "one lane per warp in the block-wide scans");
 constexpr int kEvictCluster = 8;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictCopies = 4; // histogram copies per block
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 4;    // rows per lane
+constexpr int kMoveRows = kMoveThreads; // rows per block: one place per lane
 
 struct EvictParams {
     const float *mass;      // [B][Hk][cap]
@@ -70,6 +74,14 @@ struct EvictShared {
     uint32_t total_gt, total_eq;  // this block's counts, read by the cluster
 };
 
+__device__ __forceinline__ void cluster_barrier(cooperative_groups::cluster_group &cluster, int cs)
+{
+    if (cs == 1)
+        __syncthreads();
+    else
+        cluster.sync();
+}
+
 // Digit of the wanted-th largest key among the counted ones: the bin where the running count
 // from the top reaches `wanted`. Every block of the cluster computes it from all histograms.
 __device__ __forceinline__ void pick_digit(cooperative_groups::cluster_group &cluster,
@@ -87,11 +99,24 @@ __device__ __forceinline__ void pick_digit(cooperative_groups::cluster_group &cl
         n[i] = 0;
     const int top = bins - 1 - kPer * tid;
     if (top >= 0) {
-        for (int r = 0; r < cs; ++r) {
-            const uint32_t *h = cluster.map_shared_rank(&sh.hist[buf][0], r);
+        if (cs == 1) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                n[i] += h[top - i];
+                n[i] = sh.hist[buf][top - i];
+        } else {
+            uint32_t v[kEvictCluster][kPer]; // all blocks' counts in flight at once
+#pragma unroll
+            for (int r = 0; r < kEvictCluster; ++r) {
+                const uint32_t *h = cluster.map_shared_rank(&sh.hist[buf][0], r < cs ? r : 0);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    v[r][i] = r < cs ? h[top - i] : 0;
+            }
+#pragma unroll
+            for (int r = 0; r < kEvictCluster; ++r)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    n[i] += v[r][i];
         }
     }
 #pragma unroll
@@ -107,10 +132,16 @@ __device__ __forceinline__ void pick_digit(cooperative_groups::cluster_group &cl
     if (lane == 31)
         sh.warp_sum[warp] = incl;
     __syncthreads();
-    uint32_t run = incl - sum;
+    // (one value per warp and lane: the warps' sums are added by one more warp scan)
+    uint32_t ws = sh.warp_sum[lane];
+    const uint32_t own = ws;
 #pragma unroll
-    for (int w = 0; w < kEvictWarps; ++w)
-        run += w < warp ? sh.warp_sum[w] : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, ws, o);
+        if (lane >= o)
+            ws += t;
+    }
+    uint32_t run = incl - sum + __shfl_sync(0xffffffffu, ws - own, warp);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (run < wanted && wanted <= run + n[i]) {
@@ -169,10 +200,21 @@ __global__ void __launch_bounds__(kEvictThreads)
     const int mid0 = p.sink, mid1 = L - p.recent;
     const float *src = mass + lo; // position lo + i at src[i]
     if (p.in_smem) {
-        for (int i = tid; i < hi - lo; i += kEvictThreads)
-            buf[i] = src[i];
+        const int n = hi - lo;
+        constexpr int kBatch = 16;
+#pragma unroll 1
+        for (int i0 = tid; i0 < n; i0 += kBatch * kEvictThreads) {
+            float v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (i0 + u * kEvictThreads < n)
+                    v[u] = __ldg(src + i0 + u * kEvictThreads);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (i0 + u * kEvictThreads < n)
+                    buf[i0 + u * kEvictThreads] = v[u];
+        }
         src = buf;
-        __syncthreads();
     }
 
     // ---- threshold key T, and how many tokens equal to it stay
@@ -185,11 +227,14 @@ __global__ void __launch_bounds__(kEvictThreads)
             const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
             const int bins = round == 2 ? 1024 : 2048;
             const int above = shift + (round == 2 ? 10 : 11); // bits decided so far: 32 - above
-            for (int i = tid; i < kEvictCopies * kEvictBins; i += kEvictThreads)
-                (&sh.copies[0][0])[i] = 0;
-            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kEvictCopies * kEvictBins / 4 / kEvictThreads; ++i)
+                reinterpret_cast<uint4 *>(&sh.copies[0][0])[i * kEvictThreads + tid] =
+                    make_uint4(0, 0, 0, 0);
+            __syncthreads(); // (in the first round: the masses are there, too)
             uint32_t *mine = sh.copies[lane % kEvictCopies];
             const int a = (mid0 > lo ? mid0 : lo) - lo, z = (mid1 < hi ? mid1 : hi) - lo;
+#pragma unroll 4
             for (int i = a + tid; i < z; i += kEvictThreads) {
                 const uint32_t key = mass_key(src[i]);
                 if (round == 0 || (key >> above) == prefix)
@@ -205,7 +250,7 @@ __global__ void __launch_bounds__(kEvictThreads)
                     s += sh.copies[c][i];
                 sh.hist[round & 1][i] = s;
             }
-            cluster.sync();
+            cluster_barrier(cluster, cs);
             pick_digit(cluster, sh, round & 1, bins, wanted, tid);
             prefix = (prefix << (round == 2 ? 10 : 11)) | sh.digit;
             wanted = sh.rest;
@@ -215,6 +260,8 @@ __global__ void __launch_bounds__(kEvictThreads)
     }
 
     // ---- count, then write: warp w takes a contiguous run of positions
+    if (p.keep == p.sink + p.recent)
+        __syncthreads(); // (no round above has waited for the masses)
     const int rows = (hi - lo + 31) >> 5;
     const int r0 = rows * warp / kEvictWarps, r1 = rows * (warp + 1) / kEvictWarps;
     auto classify = [&](int i, float &x, bool &gt, bool &eq) {
@@ -230,6 +277,7 @@ __global__ void __launch_bounds__(kEvictThreads)
         }
     };
     uint32_t ngt = 0, neq = 0;
+#pragma unroll 4
     for (int r = r0; r < r1; ++r) {
         float x;
         bool gt, eq;
@@ -242,24 +290,40 @@ __global__ void __launch_bounds__(kEvictThreads)
         sh.eq[warp] = neq;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t g = 0, e = 0;
-        for (int w = 0; w < kEvictWarps; ++w) {
-            g += sh.gt[w];
-            e += sh.eq[w];
+    // counts of the warps before this one, and of the block
+    uint32_t wg = sh.gt[lane], we = sh.eq[lane];
+    const uint32_t og = wg, oe = we;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t a = __shfl_up_sync(0xffffffffu, wg, o);
+        const uint32_t c = __shfl_up_sync(0xffffffffu, we, o);
+        if (lane >= o) {
+            wg += a;
+            we += c;
         }
-        sh.total_gt = g;
-        sh.total_eq = e;
     }
-    cluster.sync();
-    uint32_t gt_before = 0, eq_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        gt_before += *cluster.map_shared_rank(&sh.total_gt, r);
-        eq_before += *cluster.map_shared_rank(&sh.total_eq, r);
+    if (tid == 31) {
+        sh.total_gt = wg;
+        sh.total_eq = we;
     }
-    for (int w = 0; w < warp; ++w) {
-        gt_before += sh.gt[w];
-        eq_before += sh.eq[w];
+    uint32_t gt_before = __shfl_sync(0xffffffffu, wg - og, warp);
+    uint32_t eq_before = __shfl_sync(0xffffffffu, we - oe, warp);
+    if (cs > 1) {
+        cluster.sync();
+        uint32_t tg[kEvictCluster], te[kEvictCluster];
+#pragma unroll
+        for (int r = 0; r < kEvictCluster; ++r) {
+            tg[r] = te[r] = 0;
+            if (r < rank) {
+                tg[r] = *cluster.map_shared_rank(&sh.total_gt, r);
+                te[r] = *cluster.map_shared_rank(&sh.total_eq, r);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kEvictCluster; ++r) {
+            gt_before += tg[r];
+            eq_before += te[r];
+        }
     }
     const uint32_t below = (1u << lane) - 1u;
     for (int r = r0; r < r1; ++r) {
@@ -276,66 +340,75 @@ __global__ void __launch_bounds__(kEvictThreads)
         gt_before += __popc(mg);
         eq_before += __popc(me);
     }
-    cluster.sync(); // no block leaves while its counts are read
+    if (cs > 1)
+        cluster.sync(); // no block leaves while its counts are read
 }
 
-// Rows of sequence blockIdx.y: row r is kept token r / Hk of head r % Hk.
+// Rows of sequence blockIdx.y: row r is kept token r / Hk of head r % Hk. Quotients by the
+// head count and the block size are taken once per row.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads)
     evict_move_kernel(const __grid_constant__ EvictParams p)
 {
-    constexpr int kLanes = D / 16; // lanes per row
-    constexpr int kPerPass = kMoveThreads / kLanes;
+    constexpr int kLanes = D / 16;          // lanes per row
+    constexpr int kAtOnce = 32 / kLanes;    // rows a warp moves per instruction
+    constexpr int kBatch = kLanes < 4 ? kLanes : 4; // such steps in flight
     grid_dep_wait();
     grid_dep_launch();
     const int b = blockIdx.y;
-    const int sub = threadIdx.x % kLanes;
-    const int rows = p.keep * p.Hk; // < 2^31 (host check)
-    const int base = blockIdx.x * kPerPass * kMoveRows + threadIdx.x / kLanes;
-    const int32_t *table = p.table + (long long)b * p.mbps;
-    const int32_t *new_table = p.new_table + (long long)b * p.new_mbps;
-    long long src[kMoveRows], dst[kMoveRows]; // row indices (slot * Hk + head), src < 0: none
-    unsigned err = 0;
-#pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
-        src[i] = -1;
-        const int r = base + i * kPerPass;
-        if (r >= 0 && r < rows) {
-            const int j = r / p.Hk, h = r - j * p.Hk;
-            const int t = __ldcg(p.kept + ((long long)b * p.Hk + h) * p.keep + j);
-            if (t >= 0) {
-                const int from = __ldg(table + t / p.bs), to = __ldg(new_table + j / p.bs);
-                if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) {
-                    err |= 0x2u; // block-table entry outside the pool: the row is skipped
-                } else {
-                    src[i] = ((long long)from * p.bs + t % p.bs) * p.Hk + h;
-                    dst[i] = ((long long)to * p.bs + j % p.bs) * p.Hk + h;
-                    if (src[i] == dst[i])
-                        src[i] = -1; // in place already
-                }
+    const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
+    const unsigned rows = (unsigned)(p.keep * p.Hk); // < 2^30 (host check)
+    const unsigned r = blockIdx.x * kMoveRows + threadIdx.x;
+    long long src = -1, dst = 0; // this lane's row (slot * Hk + head); src < 0: none
+    if (r < rows) {
+        const unsigned j = r / (unsigned)p.Hk, h = r - j * (unsigned)p.Hk;
+        const int t = __ldcg(p.kept + ((long long)b * p.Hk + h) * p.keep + j);
+        if (t >= 0) {
+            const unsigned tb = (unsigned)t / (unsigned)p.bs, jb = j / (unsigned)p.bs;
+            const int from = __ldg(p.table + (long long)b * p.mbps + tb);
+            const int to = __ldg(p.new_table + (long long)b * p.new_mbps + jb);
+            if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) {
+                atomicOr(p.errors, 0x2u); // block-table entry outside the pool: skipped
+            } else {
+                src = ((long long)from * p.bs + ((unsigned)t - tb * p.bs)) * p.Hk + h;
+                dst = ((long long)to * p.bs + (j - jb * p.bs)) * p.Hk + h;
+                if (src == dst)
+                    src = -1; // in place already
             }
         }
     }
-    uint4 k[kMoveRows], v[kMoveRows];
-    float s[kMoveRows];
+    float ks = 0.f, vs = 0.f;
+    if (src >= 0) {
+        ks = p.ks[src];
+        vs = p.vs[src];
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
+        uint4 k[kBatch], v[kBatch];
+        long long d[kBatch];
 #pragma unroll
-    for (int i = 0; i < kMoveRows; ++i)
-        if (src[i] >= 0) {
-            k[i] = __ldcs(reinterpret_cast<const uint4 *>(p.k + src[i] * D) + sub);
-            v[i] = __ldcs(reinterpret_cast<const uint4 *>(p.v + src[i] * D) + sub);
-            if (sub < 2)
-                s[i] = (sub == 0 ? p.ks : p.vs)[src[i]];
+        for (int i = 0; i < kBatch; ++i) {
+            const int from = (i0 + i) * kAtOnce + grp;
+            const long long s = __shfl_sync(0xffffffffu, src, from);
+            d[i] = __shfl_sync(0xffffffffu, dst, from);
+            if (s < 0) {
+                d[i] = -1;
+            } else {
+                k[i] = __ldcs(reinterpret_cast<const uint4 *>(p.k + s * D) + sub);
+                v[i] = __ldcs(reinterpret_cast<const uint4 *>(p.v + s * D) + sub);
+            }
         }
 #pragma unroll
-    for (int i = 0; i < kMoveRows; ++i)
-        if (src[i] >= 0) {
-            *(reinterpret_cast<uint4 *>(p.k + dst[i] * D) + sub) = k[i];
-            *(reinterpret_cast<uint4 *>(p.v + dst[i] * D) + sub) = v[i];
-            if (sub < 2)
-                (sub == 0 ? p.ks : p.vs)[dst[i]] = s[i];
-        }
-    if (err)
-        atomicOr(p.errors, err);
+        for (int i = 0; i < kBatch; ++i)
+            if (d[i] >= 0) {
+                *(reinterpret_cast<uint4 *>(p.k + d[i] * D) + sub) = k[i];
+                *(reinterpret_cast<uint4 *>(p.v + d[i] * D) + sub) = v[i];
+            }
+    }
+    if (src >= 0) {
+        p.ks[dst] = ks;
+        p.vs[dst] = vs;
+    }
 }
 
 } // namespace q8kv

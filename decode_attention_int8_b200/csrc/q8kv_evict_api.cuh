@@ -14,7 +14,7 @@ bool g_evict_attr[kMaxDevices];
 template <int D>
 q8kv_status launch_move(const EvictParams &p, cudaStream_t stream)
 {
-    constexpr int per_block = kMoveThreads / (D / 16) * kMoveRows;
+    constexpr int per_block = kMoveRows;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -104,11 +104,11 @@ q8kv_status q8kv_evict(int8_t *k_blocks, int8_t *v_blocks, float *kscale, float 
     p.cap = max_blocks_per_seq * kv_block_size;
     p.new_cap = new_max_blocks_per_seq * kv_block_size;
     p.errors = dev->errors;
-    // Blocks per (sequence, head): more while the machine has room for them (2 blocks per SM)
-    // and each still has 1024 positions or more.
+    // Blocks per (sequence, head): one for up to 16 masses per thread, more for longer rows
+    // while the machine has room for them (a block per SM).
     const long long pairs = (long long)B * n_kv_heads;
     int cs = 1;
-    while (cs < kEvictCluster && pairs * cs * 2 <= 2LL * dev->sms && p.cap > 1024 * cs)
+    while (cs < kEvictCluster && pairs * cs * 2 <= dev->sms && p.cap > 16 * kEvictThreads * cs)
         cs *= 2;
     // and as many as it takes for a block's masses to fit its shared memory
     auto part = [&](int n) { return ((size_t)((p.cap + n - 1) / n + 31) & ~(size_t)31) * 4; };

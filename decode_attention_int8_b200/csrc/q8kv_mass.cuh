@@ -15,7 +15,8 @@
 // lanes c = 2, 3 block 2h + 1, and the query operand is zero where column group n / 4 and block
 // differ. One accumulator so carries two blocks' exact dots side by side, every column is
 // used, and two shuffles bring the halves together, each lane keeping two rows of one token.
-// A loop iteration has the next 16 tokens' rows, scale and mass in flight. The tokens of all
+// Two register sets alternate, so the next 16 tokens' rows, scale and mass are in flight while
+// one set is used, and the first ones while the query is quantised. The tokens of all
 // sequences form one list that the blocks share evenly; a block's warps take different heads of
 // the same tokens, whose rows are neighbours in the pool.
 #pragma once
@@ -51,11 +52,10 @@ struct MassQuad {
     uint32_t b[2][4];  // [half][words of the lane's 16 bytes]
     float qs[2][2];    // [half][row]: scale of the lane's block
     float lse2[2];
-    int lim[2];        // the rows' views: tokens below lim
 };
 
-__device__ __forceinline__ MassQuad mass_query(const MassParams &p, int b, int kv, int row0, int L,
-                                               int g, int c)
+__device__ __forceinline__ MassQuad mass_query(const MassParams &p, int b, int kv, int row0, int g,
+                                               int c)
 {
     MassQuad f;
     const int r = row0 + (g & 3); // column g of the operand
@@ -107,13 +107,11 @@ __device__ __forceinline__ MassQuad mass_query(const MassParams &p, int b, int k
         for (int h = 0; h < 2; ++h)
             f.qs[h][e] = __shfl_sync(kFullMask, qsc[h], from);
         const int rr = row0 + 2 * (c & 1) + e;
-        f.lse2[e] = 0.f;
-        f.lim[e] = 0; // a padding row sees nothing
+        f.lse2[e] = INFINITY; // a padding row weighs nothing: exp2(0 - inf)
         if (rr < p.R) {
             const int i = rr / p.Gq;
             f.lse2[e] = __ldg(p.lse + ((long long)b * p.nq + i) * p.Hq + (long long)kv * p.Gq +
                               (rr - i * p.Gq)) * 1.44269504088896341f;
-            f.lim[e] = L - (p.nq - 1 - i);
         }
     }
     return f;
@@ -183,6 +181,8 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, NQ == 4 ? 2 : 3)
     const int hw = warp % p.heads_pass, sub = warp / p.heads_pass;
     const int bs_mask = (1 << p.bs_log2) - 1;
     const int sel = c >> 1; // which half of the tile's tokens this lane keeps
+    const bool writer = (c & 1) == 0;
+    const unsigned row8 = 8u * (unsigned)p.Hk * kD; // bytes from token t's row to t + 8's
 
     while (t0 < t1) {
         // the sequence of tile t0: the last b with prefix[b] <= t0
@@ -199,70 +199,68 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, NQ == 4 ? 2 : 3)
         int L = __ldg(p.lens + b);
         L = L > p.cap ? p.cap : L;
         const int32_t *table = p.table + (long long)b * p.mbps;
-        const int sees_all = L - (p.nq - 1); // tokens every row sees
+        const int all_see = L - (p.nq - 1); // tokens that every row sees
+        const int tok1 = (t2 - first) * kMassTile;
 #pragma unroll 1
         for (int kv = hw; kv < p.Hk; kv += p.heads_pass) {
-            float *mass = p.mass + ((long long)b * p.Hk + kv) * p.cap;
+            float *mass = p.mass + ((long long)b * p.Hk + kv) * p.cap + g + 8 * sel;
+            const int8_t *kbase = p.k + ((long long)g * p.Hk + kv) * kD + 16 * c;
+            const float *sbase = p.ks + (long long)(g + 8 * sel) * p.Hk + kv;
 #pragma unroll 1
             for (int row0 = 0; row0 < p.R; row0 += 4 * NQ) {
-                MassQuad q[NQ];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-                    q[n] = mass_query(p, b, kv, row0 + 4 * n, L, g, c);
                 const float decay = row0 == 0 ? p.decay : 1.f;
+                const int step = p.subs * kMassTile;
+                int t = (t0 - first + sub) * kMassTile; // first token of the tile
 
-                auto load = [&](int tile) {
-                    MassTile m;
-                    const int t = (tile - first) * kMassTile;
+                auto load = [&](MassTile &m, int t) {
                     const int blk = __ldg(table + (t >> p.bs_log2));
-                    m.ok = blk >= 0 && blk < p.num_blocks;
-                    const long long slot = ((long long)(m.ok ? blk : 0) << p.bs_log2) + (t & bs_mask);
+                    m.ok = (unsigned)blk < (unsigned)p.num_blocks;
                     if (!m.ok && lane == 0)
                         atomicOr(p.errors, kErrBlockTable);
-                    const int8_t *row = p.k + ((slot + g) * p.Hk + kv) * kD + 16 * c;
-                    const long long next8 = 8LL * p.Hk * kD;
+                    const int slot = ((m.ok ? blk : 0) << p.bs_log2) + (t & bs_mask);
+                    const long long row = (long long)slot * p.Hk; // (slot, head 0)
+                    const int8_t *k = kbase + row * kD;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            m.k[u][h] = __ldcs(
-                                reinterpret_cast<const uint4 *>(row + u * next8 + 64 * h));
-                    m.ks = __ldg(p.ks + (slot + g + 8 * sel) * p.Hk + kv);
+                            m.k[u][h] =
+                                __ldcs(reinterpret_cast<const uint4 *>(k + u * row8 + 64 * h));
+                    m.ks = __ldg(sbase + row);
                     m.old = 0.f;
-                    if (decay != 0.f && (c & 1) == 0 && t + g + 8 * sel < L)
-                        m.old = mass[t + g + 8 * sel];
-                    return m;
+                    if (decay != 0.f && writer && t + g + 8 * sel < L)
+                        m.old = mass[t];
                 };
-                int tile = t0 + sub;
-                MassTile cur;
-                if (tile < t2 && sub < p.subs)
-                    cur = load(tile);
-                else
-                    tile = t2;
-#pragma unroll 1
-                for (; tile < t2; tile += p.subs) {
-                    MassTile next = cur;
-                    if (tile + p.subs < t2)
-                        next = load(tile + p.subs);
-                    const int tok0 = (tile - first) * kMassTile;
-                    const int tok = tok0 + g + 8 * sel;
-                    const float ksl = cur.ks * p.scale_log2;
+                MassTile A, B;
+                if (t < tok1)
+                    load(A, t);
+                MassQuad q[NQ];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    q[n] = mass_query(p, b, kv, row0 + 4 * n, g, c);
+
+                auto use = [&](const MassTile &m, int t) {
+                    const float ksl = m.ks * p.scale_log2;
+                    const int tok = t + g + 8 * sel;
                     float w = 0.f;
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}}; // [token half][row]
+                        float s[2][2]; // [token half][row]
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             int d[4];
-                            const uint4 x = cur.k[0][h], y = cur.k[1][h];
+                            const uint4 x = m.k[0][h], y = m.k[1][h];
                             mma_s8_16832_biased(d, x.x, y.x, x.y, y.y, q[n].b[h][0], q[n].b[h][1]);
                             mma_s8_16832_acc(d, x.z, y.z, x.w, y.w, q[n].b[h][2], q[n].b[h][3], d);
 #pragma unroll
                             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) // the biased view minus the bias: exact
-                                    s[u][e] = fmaf(__int_as_float(d[2 * u + e]) - kDotBiasF,
-                                                   q[n].qs[h][e], s[u][e]);
+                                for (int e = 0; e < 2; ++e) {
+                                    // the biased view minus the bias: exact
+                                    const float v = __int_as_float(d[2 * u + e]) - kDotBiasF;
+                                    s[u][e] = h == 0 ? v * q[n].qs[0][e]
+                                                     : fmaf(v, q[n].qs[1][e], s[u][e]);
+                                }
                         }
                         // blocks 0, 2 lie in lanes c < 2 and blocks 1, 3 in lanes c >= 2 (of
                         // the same rows): each lane gives the token it does not keep
@@ -272,16 +270,31 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, NQ == 4 ? 2 : 3)
                             const float keep = sel ? s[1][e] : s[0][e];
                             const float x = keep + __shfl_xor_sync(kFullMask, give, 2);
                             const float a = fast_exp2(fmaf(x, ksl, -q[n].lse2[e]));
-                            if (tok0 + kMassTile <= sees_all)
-                                w += q[n].lim[e] > 0 ? a : 0.f;
-                            else
-                                w += tok < q[n].lim[e] ? a : 0.f;
+                            if (t + kMassTile <= all_see) {
+                                w += a;
+                            } else { // row r sees the tokens below L - (nq - 1 - r / Gq)
+                                const int r = row0 + 4 * n + 2 * (c & 1) + e;
+                                w += tok < all_see + r / p.Gq ? a : 0.f;
+                            }
                         }
                     }
                     w += __shfl_xor_sync(kFullMask, w, 1);
-                    if ((c & 1) == 0 && tok < L && cur.ok)
-                        mass[tok] = decay == 0.f ? w : fmaf(decay, cur.old, w);
-                    cur = next;
+                    if (writer && tok < L && m.ok)
+                        mass[t] = decay == 0.f ? w : fmaf(decay, m.old, w);
+                };
+                while (t < tok1) {
+                    int tn = t + step;
+                    if (tn < tok1)
+                        load(B, tn);
+                    use(A, t);
+                    t = tn;
+                    if (t >= tok1)
+                        break;
+                    tn = t + step;
+                    if (tn < tok1)
+                        load(A, tn);
+                    use(B, t);
+                    t = tn;
                 }
             }
         }

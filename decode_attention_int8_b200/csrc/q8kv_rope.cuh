@@ -12,13 +12,14 @@
 // are then quantised by the row rule of q8kv_cache_write.cuh.
 //
 // What bounds it: HBM. A token reads (Hq + 2 Hk) D elements and writes 4 Hq D + 2 Hk (D + 4)
-// bytes; a separate rotation would write and read the keys once more. The table rows are
-// shared by a token's Hq + Hk rotated rows, so a warp takes the rows of one token one after
-// the other and keeps the cosines and sines of its lanes' pairs in registers: a row has 8
-// lanes (16 for head_dim 256) of 4-element chunks, as in the cache write, so 4 (or 2) rows
-// go at once, and with rotary_dim = head_dim and pairs (p, p + D / 2) both members of a pair
-// lie in one lane. Few tokens leave most of the machine empty when a warp takes a whole token,
-// so a token's rows are then split over several warps (rope_parts).
+// bytes; a separate rotation would write and read the keys once more. A block takes a tile of
+// up to 4 tokens: it first gathers the tile's cosines and sines into shared memory (one thread
+// per pair, whatever its axis), then its warps stream the tile's rows, 4 (or 2) rows of 8 (16)
+// lanes at once as in the cache write, each warp with the next rows in flight. Neighbouring
+// warps take neighbouring rows, so the block reads and writes contiguous memory. (A first
+// version gave a warp one token and kept its angles in registers: 24 warps per SM at distant
+// addresses, waiting on every token's position -> table chain, ran the 32768-token fp32 prompt
+// in 632 us.) Few tokens leave SMs empty, so a tile's rows are then split over several blocks.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,7 +47,7 @@ struct RopeParams {
     long long q_stride, kv_stride; // elements from one token's rows to the next token's
     long long n_slots;
     int Hq, Hk, rot, max_pos, n_axes;
-    int parts;      // warps per token
+    int tile, parts; // tokens per block and step; blocks that share a tile
     unsigned *errors;
     uint8_t axis[128]; // axis of each pair
 };
@@ -109,81 +110,6 @@ __device__ __forceinline__ float4 rot_hi4(float4 b, float4 a, float4 c, float4 s
                        rot_hi(b.z, a.z, c.z, s.z), rot_hi(b.w, a.w, c.w, s.w));
 }
 
-// A lane's cosines and sines for one token: kRopeFull keeps the pairs of its first C / 2
-// chunks, kRopeHalf those of each chunk, kRopeAdjacent the two pairs of each chunk (in c4's
-// x, y and s4's x, y).
-template <int D, int MODE>
-struct Angles {
-    static constexpr int C = RowFrag<D>::C;
-    static constexpr int N = MODE == kRopeFull ? C / 2 : C;
-    float4 c[N], s[N];
-};
-
-__device__ __forceinline__ int axis_pos(const int (&pos)[kRopeAxes], int a)
-{
-    int r = pos[0];
-#pragma unroll
-    for (int i = 1; i < kRopeAxes; ++i)
-        r = a == i ? pos[i] : r;
-    return r;
-}
-
-// Cosines (and sines) of the 4 pairs p .. p + 3 (p a multiple of 4).
-__device__ __forceinline__ void angles4(const RopeParams &p, const int (&pos)[kRopeAxes], int pair,
-                                        float4 &c, float4 &s)
-{
-    const uint32_t a = *reinterpret_cast<const uint32_t *>(p.axis + pair);
-    const int half = p.rot >> 1;
-    if (a == (a & 0xffu) * 0x01010101u) { // one axis for all four
-        const float *row = p.table + (long long)axis_pos(pos, a & 0xffu) * p.rot + pair;
-        c = __ldg(reinterpret_cast<const float4 *>(row));
-        s = __ldg(reinterpret_cast<const float4 *>(row + half));
-        return;
-    }
-    float cc[4], ss[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float *row =
-            p.table + (long long)axis_pos(pos, (a >> (8 * i)) & 0xffu) * p.rot + pair + i;
-        cc[i] = __ldg(row);
-        ss[i] = __ldg(row + half);
-    }
-    c = make_float4(cc[0], cc[1], cc[2], cc[3]);
-    s = make_float4(ss[0], ss[1], ss[2], ss[3]);
-}
-
-template <int D, int MODE>
-__device__ __forceinline__ Angles<D, MODE> load_angles(const RopeParams &p,
-                                                       const int (&pos)[kRopeAxes], int sub)
-{
-    constexpr int LPR = write_lanes_per_row(D);
-    Angles<D, MODE> a;
-    const int half = p.rot >> 1;
-#pragma unroll
-    for (int i = 0; i < Angles<D, MODE>::N; ++i) {
-        const int e = 4 * (sub + LPR * i); // first channel of the chunk
-        a.c[i] = make_float4(1.f, 1.f, 1.f, 1.f);
-        a.s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if constexpr (MODE == kRopeAdjacent) {
-            if (e < p.rot) {
-                const int pair = e >> 1;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float *row =
-                        p.table + (long long)axis_pos(pos, p.axis[pair + k]) * p.rot + pair + k;
-                    const float c = __ldg(row), s = __ldg(row + half);
-                    (k ? a.c[i].y : a.c[i].x) = c;
-                    (k ? a.s[i].y : a.s[i].x) = s;
-                }
-            }
-        } else {
-            if (e < p.rot)
-                angles4(p, pos, MODE == kRopeHalf && e >= half ? e - half : e, a.c[i], a.s[i]);
-        }
-    }
-    return a;
-}
-
 // One row as loaded by its lanes: its chunks and, for kRopeHalf, the chunks of their partners.
 template <int D, typename T, int MODE>
 struct RopeRow {
@@ -211,9 +137,10 @@ __device__ __forceinline__ RopeRow<D, T, MODE> load_row(const T *row, int sub, i
     return r;
 }
 
+// The rotated row; cosines and sines of the token's pairs lie at cs and cs + half.
 template <int D, typename T, int MODE>
-__device__ __forceinline__ RowFrag<D> rotate(const RopeRow<D, T, MODE> &r,
-                                             const Angles<D, MODE> &a, int sub, int rot, bool turn)
+__device__ __forceinline__ RowFrag<D> rotate(const RopeRow<D, T, MODE> &r, const float *cs, int sub,
+                                             int rot, bool turn)
 {
     constexpr int LPR = write_lanes_per_row(D);
     constexpr int C = RowFrag<D>::C;
@@ -223,31 +150,41 @@ __device__ __forceinline__ RowFrag<D> rotate(const RopeRow<D, T, MODE> &r,
         f.x[c] = widen<T>(r.x[c]);
     if (!turn)
         return f;
+    const float *sn = cs + (rot >> 1);
     if constexpr (MODE == kRopeFull) {
 #pragma unroll
         for (int c = 0; c < C / 2; ++c) {
+            const int e = 4 * (sub + LPR * c);
+            const float4 co = *reinterpret_cast<const float4 *>(cs + e);
+            const float4 si = *reinterpret_cast<const float4 *>(cs + D / 2 + e);
             const float4 lo = f.x[c], hi = f.x[c + C / 2];
-            f.x[c] = rot_lo4(lo, hi, a.c[c], a.s[c]);
-            f.x[c + C / 2] = rot_hi4(hi, lo, a.c[c], a.s[c]);
+            f.x[c] = rot_lo4(lo, hi, co, si);
+            f.x[c + C / 2] = rot_hi4(hi, lo, co, si);
         }
     } else if constexpr (MODE == kRopeHalf) {
+        const int half = rot >> 1;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = 4 * (sub + LPR * c);
+            if (e >= rot)
+                continue;
+            const bool low = e < half;
             const float4 y = widen<T>(r.y[c]);
-            if (e < (rot >> 1))
-                f.x[c] = rot_lo4(f.x[c], y, a.c[c], a.s[c]);
-            else if (e < rot)
-                f.x[c] = rot_hi4(f.x[c], y, a.c[c], a.s[c]);
+            const float4 co = *reinterpret_cast<const float4 *>(cs + (low ? e : e - half));
+            const float4 si = *reinterpret_cast<const float4 *>(sn + (low ? e : e - half));
+            f.x[c] = low ? rot_lo4(f.x[c], y, co, si) : rot_hi4(f.x[c], y, co, si);
         }
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (4 * (sub + LPR * c) < rot) {
-                const float4 x = f.x[c], cc = a.c[c], ss = a.s[c];
-                f.x[c] = make_float4(rot_lo(x.x, x.y, cc.x, ss.x), rot_hi(x.y, x.x, cc.x, ss.x),
-                                     rot_lo(x.z, x.w, cc.y, ss.y), rot_hi(x.w, x.z, cc.y, ss.y));
-            }
+            const int e = 4 * (sub + LPR * c);
+            if (e >= rot)
+                continue;
+            const float4 x = f.x[c];
+            const float2 co = *reinterpret_cast<const float2 *>(cs + (e >> 1));
+            const float2 si = *reinterpret_cast<const float2 *>(sn + (e >> 1));
+            f.x[c] = make_float4(rot_lo(x.x, x.y, co.x, si.x), rot_hi(x.y, x.x, co.x, si.x),
+                                 rot_lo(x.z, x.w, co.y, si.y), rot_hi(x.w, x.z, co.y, si.y));
         }
     }
     return f;
@@ -260,6 +197,8 @@ __host__ __device__ constexpr int rope_iters(int Hq, int Hk, int D)
     return (Hq + ppw - 1) / ppw + (2 * Hk + ppw - 1) / ppw;
 }
 
+constexpr int kRopeTile = 4; // tokens per block and step, at most
+
 template <int D, typename T, int MODE>
 __global__ void __launch_bounds__(kWriteThreads, 3)
     rope_cache_write_kernel(const __grid_constant__ RopeParams p)
@@ -267,14 +206,17 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
     constexpr int LPR = write_lanes_per_row(D);
     constexpr int PPW = write_pairs_per_warp(D);
     constexpr int C = RowFrag<D>::C;
+    __shared__ __align__(16) float angle[kRopeTile][D]; // cosines, then sines, of a token
+    __shared__ long long tile_slot[kRopeTile];
     // the new rows may come from the kernel before this one on the stream
     grid_dep_wait();
     grid_dep_launch();
-    const int lane = threadIdx.x & 31, sub = lane % LPR, grp = lane / LPR;
-    const long long items = p.n_tokens * p.parts;
-    const long long step = (long long)gridDim.x * kWriteWarps;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int sub = lane % LPR, grp = lane / LPR;
     const int q_iters = (p.Hq + PPW - 1) / PPW;
     const int iters = rope_iters(p.Hq, p.Hk, D);
+    const int half = p.rot >> 1;
+    const long long units = (p.n_tokens + p.tile - 1) / p.tile * p.parts;
     unsigned err = 0;
 
     // this lane's row of iteration it of token `tok`: where it starts, whether it exists
@@ -295,55 +237,69 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
     };
 
 #pragma unroll 1
-    for (long long item = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5); item < items;
-         item += step) {
-        const long long tok = item / p.parts;
-        const int part = (int)(item - tok * p.parts);
-        const int it0 = part * iters / p.parts, it1 = (part + 1) * iters / p.parts;
-        bool exists, turn;
+    for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const long long tok0 = unit / p.parts * p.tile;
+        const int part = (int)(unit % p.parts);
+        const int nt = p.n_tokens - tok0 < p.tile ? (int)(p.n_tokens - tok0) : p.tile;
+        const int all = nt * iters; // iterations of the tile, token by token
+        int j = part * all / p.parts + warp;
+        const int j1 = (part + 1) * all / p.parts;
+        int tk = j / iters, it = j - tk * iters;
+        bool exists = false, turn = false;
         RopeRow<D, T, MODE> cur;
-        {
-            const T *row = row_of(tok, it0, exists, turn);
-            cur = load_row<D, T, MODE>(row, sub, p.rot, turn);
-        }
-        int pos[kRopeAxes];
-#pragma unroll
-        for (int a = 0; a < kRopeAxes; ++a) {
-            int x = a < p.n_axes ? __ldg(p.pos + a * p.n_tokens + tok) : 0;
-            if (x < 0 || x >= p.max_pos) {
-                err |= kErrPosition;
-                x = x < 0 ? 0 : p.max_pos - 1;
+        if (j < j1) // in flight while the angles are gathered
+            cur = load_row<D, T, MODE>(row_of(tok0 + tk, it, exists, turn), sub, p.rot, turn);
+        for (int t = 0; t < nt; ++t) {
+            if (tid < half) {
+                int x = __ldg(p.pos + (long long)p.axis[tid] * p.n_tokens + tok0 + t);
+                if (x < 0 || x >= p.max_pos) {
+                    err |= kErrPosition;
+                    x = x < 0 ? 0 : p.max_pos - 1;
+                }
+                const float *row = p.table + (long long)x * p.rot + tid;
+                angle[t][tid] = __ldg(row);
+                angle[t][half + tid] = __ldg(row + half);
             }
-            pos[a] = x;
         }
-        long long slot = __ldg(p.slots + tok);
-        if (slot >= p.n_slots) {
-            err |= kErrSlot;
-            slot = -1;
+        if (tid >= kWriteThreads - kRopeTile && tid - (kWriteThreads - kRopeTile) < nt) {
+            const int t = tid - (kWriteThreads - kRopeTile);
+            long long slot = __ldg(p.slots + tok0 + t);
+            if (slot >= p.n_slots) {
+                err |= kErrSlot;
+                slot = -1;
+            }
+            tile_slot[t] = slot;
         }
-        const Angles<D, MODE> ang = load_angles<D, MODE>(p, pos, sub);
+        __syncthreads();
 #pragma unroll 1
-        for (int it = it0; it < it1; ++it) {
+        for (; j < j1; j += kWriteWarps) {
             // the next rows are in flight while this iteration's are turned and stored
+            const long long tok = tok0 + tk;
+            const int t = tk, i = it;
+            it += kWriteWarps;
+            while (it >= iters) {
+                it -= iters;
+                ++tk;
+            }
             bool next_exists = false, next_turn = false;
             RopeRow<D, T, MODE> next = cur;
-            if (it + 1 < it1) {
-                const T *row = row_of(tok, it + 1, next_exists, next_turn);
-                next = load_row<D, T, MODE>(row, sub, p.rot, next_turn);
-            }
-            const RowFrag<D> f = rotate<D, T, MODE>(cur, ang, sub, p.rot, turn);
-            if (it < q_iters) {
+            if (j + kWriteWarps < j1)
+                next = load_row<D, T, MODE>(row_of(tok0 + tk, it, next_exists, next_turn), sub,
+                                            p.rot, next_turn);
+            const RowFrag<D> f = rotate<D, T, MODE>(cur, angle[t], sub, p.rot, turn);
+            if (i < q_iters) {
                 if constexpr (MODE == kRopeHalf)
                     __syncwarp(); // in place: every lane has read its partners
                 if (exists) {
-                    float4 *dst = reinterpret_cast<float4 *>(
-                        p.q_out + (tok * p.Hq + it * PPW + grp) * D);
+                    float4 *dst =
+                        reinterpret_cast<float4 *>(p.q_out + (tok * p.Hq + i * PPW + grp) * D);
 #pragma unroll
                     for (int c = 0; c < C; ++c)
                         dst[sub + LPR * c] = f.x[c];
                 }
             } else {
-                const int r = (it - q_iters) * PPW + grp;
+                const int r = (i - q_iters) * PPW + grp;
+                const long long slot = tile_slot[t];
                 const bool store = exists && slot >= 0;
                 const long long row = store ? slot * p.Hk + (turn ? r : r - p.Hk) : 0;
                 bool bad;
@@ -360,6 +316,7 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
             exists = next_exists;
             turn = next_turn;
         }
+        __syncthreads(); // the angles are written again
     }
     if (err)
         atomicOr(p.errors, err);

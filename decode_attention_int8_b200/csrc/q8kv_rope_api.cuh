@@ -34,15 +34,17 @@ q8kv_status launch_pdl(void (*fn)(Params), const Params &p, unsigned grid, unsig
 template <int D, typename T>
 q8kv_status launch_rope(RopeParams &p, int mode, int sms, cudaStream_t stream)
 {
-    // Warps per token: a whole token per warp reads the table row once, but leaves SMs empty
-    // for few tokens; then a token's iterations are spread until a wave (3 blocks of 8 warps
-    // per SM) is full.
+    // Four tokens per block step when they fill a wave (3 blocks per SM), else one; a tile that
+    // still leaves SMs empty is shared by several blocks, of at least one row group per warp.
     const int iters = rope_iters(p.Hq, p.Hk, D);
-    const long long wave = 3LL * sms * kWriteWarps;
-    long long parts = (wave + p.n_tokens - 1) / p.n_tokens;
-    p.parts = (int)(parts < iters ? parts : iters);
-    const long long blocks = (p.n_tokens * p.parts + kWriteWarps - 1) / kWriteWarps;
-    const unsigned grid = (unsigned)(blocks < 3LL * sms ? blocks : 3LL * sms);
+    const long long wave = 3LL * sms;
+    p.tile = p.n_tokens >= kRopeTile * wave ? kRopeTile : 1;
+    const long long tiles = (p.n_tokens + p.tile - 1) / p.tile;
+    const long long most = (iters * p.tile + kWriteWarps - 1) / kWriteWarps;
+    const long long parts = (wave + tiles - 1) / tiles;
+    p.parts = (int)(parts < most ? parts : most);
+    const long long blocks = tiles * p.parts;
+    const unsigned grid = (unsigned)(blocks < wave ? blocks : wave);
     if (mode == kRopeFull)
         return launch_pdl(rope_cache_write_kernel<D, T, kRopeFull>, p, grid, kWriteThreads, 0,
                           stream);

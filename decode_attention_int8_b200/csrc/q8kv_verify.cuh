@@ -30,7 +30,7 @@
 namespace q8kv {
 
 constexpr unsigned kErrProbs = 0x80u; // a draft token, draft count or row of weights was unusable
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;
 
@@ -82,13 +82,14 @@ __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
 // above zero, NaN among it, weighs nothing.
 enum VerifyMode { kPlain = 0, kResidual = 1, kWithout = 2 };
 
-__device__ __forceinline__ double weight(int mode, float p, float q, int x, int without)
+template <int MODE>
+__device__ __forceinline__ double weight(float p, float q, int x, int without)
 {
     double w = (double)p;
-    if (mode == kResidual)
+    if constexpr (MODE == kResidual)
         w -= (double)q;
-    else if (mode == kWithout && x == without)
-        w = 0.0;
+    else if constexpr (MODE == kWithout)
+        w = x == without ? 0.0 : w;
     return w > 0.0 ? w : 0.0;
 }
 
@@ -112,44 +113,59 @@ __device__ __forceinline__ double warp_scan(double x, int lane)
 }
 
 // Sum of the weights of tokens [lo, hi), one warp (lo a multiple of VEC).
+template <typename T, int VEC, int MODE>
+__device__ __forceinline__ double piece_sum_mode(const T *pr, const T *qr, int without, int lo,
+                                                 int hi, int lane)
+{
+    constexpr int U = VEC == 1 ? 8 : (VEC == 4 ? 4 : 2); // packs of each row in flight per lane
+    constexpr int kStep = 32 * VEC;
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    int e0 = lo + lane * VEC;
+#pragma unroll 1
+    for (; e0 + (U - 1) * kStep + VEC <= hi; e0 += U * kStep) { // (lanes may differ by one turn)
+        Pack<T, VEC> a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            a[u] = load_pack<T, VEC>(pr + e0 + u * kStep);
+            if constexpr (MODE == kResidual)
+                b[u] = load_pack<T, VEC>(qr + e0 + u * kStep);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                acc[(u * VEC + i) & 3] +=
+                    weight<MODE>(as_f32(a[u].v[i]), MODE == kResidual ? as_f32(b[u].v[i]) : 0.f,
+                                 e0 + u * kStep + i, without);
+    }
+#pragma unroll 1
+    for (; e0 < hi; e0 += kStep)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (e0 + i < hi)
+                acc[i & 3] += weight<MODE>(as_f32(pr[e0 + i]),
+                                           MODE == kResidual ? as_f32(qr[e0 + i]) : 0.f, e0 + i,
+                                           without);
+    return warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ double piece_sum(const T *pr, const T *qr, int mode, int without, int lo,
                                             int hi, int lane)
 {
-    constexpr int U = VEC == 1 ? 8 : (VEC == 4 ? 4 : 2); // packs of each row in flight per lane
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 1
-    for (int e0 = lo + lane * VEC; e0 < hi; e0 += 32 * VEC * U) {
-        Pack<T, VEC> a[U], b[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int e = e0 + 32 * VEC * u;
-            if (e < hi) {
-                a[u] = load_pack<T, VEC>(pr + e);
-                if (mode == kResidual)
-                    b[u] = load_pack<T, VEC>(qr + e);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int e = e0 + 32 * VEC * u;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (e + i < hi)
-                    acc[(u * VEC + i) & 3] +=
-                        weight(mode, as_f32(a[u].v[i]),
-                               mode == kResidual ? as_f32(b[u].v[i]) : 0.f, e + i, without);
-        }
-    }
-    return warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    if (mode == kResidual)
+        return piece_sum_mode<T, VEC, kResidual>(pr, qr, without, lo, hi, lane);
+    if (mode == kPlain)
+        return piece_sum_mode<T, VEC, kPlain>(pr, qr, without, lo, hi, lane);
+    return piece_sum_mode<T, VEC, kWithout>(pr, qr, without, lo, hi, lane);
 }
 
 // The token of piece [lo, hi): the first whose running sum, counted from `base`, exceeds
 // `goal`, or the last of any weight when rounding leaves none. Each lane sums a contiguous
-// part; the part that crosses the goal is halved down to 32 tokens in the same way.
-template <typename T>
-__device__ int piece_find(const T *pr, const T *qr, int mode, int without, int lo, int hi,
-                          double base, double goal, int lane)
+// part; the part that crosses the goal is divided in the same way, down to one token.
+template <typename T, int MODE>
+__device__ int piece_find_mode(const T *pr, const T *qr, int without, int lo, int hi, double base,
+                               double goal, int lane)
 {
 #pragma unroll 1
     for (;;) {
@@ -157,9 +173,23 @@ __device__ int piece_find(const T *pr, const T *qr, int mode, int without, int l
         const int a = lo + lane * part < hi ? lo + lane * part : hi;
         const int b = a + part < hi ? a + part : hi;
         double s = 0.0;
-#pragma unroll 4
-        for (int e = a; e < b; ++e)
-            s += weight(mode, as_f32(pr[e]), mode == kResidual ? as_f32(qr[e]) : 0.f, e, without);
+        constexpr int U = 16;
+#pragma unroll 1
+        for (int e = a; e < b; e += U) {
+            float x[U], y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[u] = y[u] = 0.f;
+                if (e + u < b) {
+                    x[u] = as_f32(pr[e + u]);
+                    if constexpr (MODE == kResidual)
+                        y[u] = as_f32(qr[e + u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                s += weight<MODE>(x[u], y[u], e + u, without);
+        }
         const double incl = base + warp_scan(s, lane);
         unsigned at = __ballot_sync(0xffffffffu, incl > goal && s > 0.0);
         int sel;
@@ -177,8 +207,19 @@ __device__ int piece_find(const T *pr, const T *qr, int mode, int without, int l
     }
 }
 
+template <typename T>
+__device__ __forceinline__ int piece_find(const T *pr, const T *qr, int mode, int without, int lo,
+                                          int hi, double base, double goal, int lane)
+{
+    if (mode == kResidual)
+        return piece_find_mode<T, kResidual>(pr, qr, without, lo, hi, base, goal, lane);
+    if (mode == kPlain)
+        return piece_find_mode<T, kPlain>(pr, qr, without, lo, hi, base, goal, lane);
+    return piece_find_mode<T, kWithout>(pr, qr, without, lo, hi, base, goal, lane);
+}
+
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kVerifyThreads)
+__global__ void __launch_bounds__(kVerifyThreads, 4)
     verify_kernel(const __grid_constant__ VerifyParams p)
 {
     namespace cg = cooperative_groups;

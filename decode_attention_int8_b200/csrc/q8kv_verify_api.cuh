@@ -41,7 +41,7 @@ q8kv_status launch_verify(const VerifyParams &p, int B, int sms, cudaStream_t st
     // 16-byte loads where every row starts on 16 bytes
     const bool vec = aligned16(p.target) && p.target_stride % kVec == 0 &&
                      (!p.draft || (aligned16(p.draft) && p.draft_stride % kVec == 0));
-    // blocks per sequence: as many as one wave holds (4 blocks of 512 threads per SM)
+    // blocks per sequence: as many as one wave holds (4 blocks per SM)
     int cs = kVerifyCluster;
     while (cs > 1 && (long long)B * cs > 4LL * sms)
         cs /= 2;
