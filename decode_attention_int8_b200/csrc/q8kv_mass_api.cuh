@@ -14,19 +14,22 @@ bool g_mass_attr[kMaxDevices][3];
 template <int NQ>
 q8kv_status launch_mass(const MassParams &p, DeviceInfo *dev, int warps, cudaStream_t stream)
 {
-    bool &set = g_mass_attr[dev - g_dev][NQ == 4 ? 2 : NQ - 1];
-    const size_t smem = sizeof(int) * ((size_t)p.B + 1);
+    bool &set = g_mass_attr[dev - g_dev][NQ];
     {
         std::lock_guard<std::mutex> lock(g_mutex);
         if (!set) {
             Q8KV_CUDA(cudaFuncSetAttribute(attn_mass_kernel<NQ>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)(sizeof(int) * (kMassMaxBatch + 1))));
+                                           dev->smem_optin - 1024));
             set = true;
         }
     }
+    const uint32_t smem = mass_layout(warps, p.heads_pass, p.quads, p.B).total;
+    // as many blocks as one wave holds: 3 per SM (24 warps), fewer with many query rows or
+    // sequences
+    long long wave = (long long)(dev->smem_optin / (smem + 1024));
+    wave = (wave < 1 ? 1 : (wave > 3 ? 3 : wave)) * dev->sms;
     const long long tiles = (long long)p.B * ((p.cap + kMassTile - 1) / kMassTile);
-    const long long wave = (NQ == 4 ? 2LL : 3LL) * dev->sms;
     return launch_pdl(attn_mass_kernel<NQ>, p, (unsigned)(tiles < wave ? tiles : wave),
                       (unsigned)warps * 32u, smem, stream);
 }
@@ -56,7 +59,7 @@ q8kv_status q8kv_attn_mass(float *mass, const float *q, const float *lse, const 
         return Q8KV_ERR_INVALID_ARG;
     const long long R = (long long)n_queries * (n_q_heads / n_kv_heads);
     if (head_dim != kD || !is_pow2(kv_block_size) || kv_block_size < 16 || kv_block_size > 256 ||
-        R > 128 || B > kMassMaxBatch || n_kv_heads > 4096 ||
+        R > kMassMaxRows || B > kMassMaxBatch || n_kv_heads > 4096 ||
         (long long)num_kv_blocks * kv_block_size >= (1LL << 31) ||
         (long long)max_blocks_per_seq * kv_block_size >= (1LL << 30) ||
         (long long)B * max_blocks_per_seq * (kv_block_size / 16) >= (1LL << 31))
@@ -90,17 +93,21 @@ q8kv_status q8kv_attn_mass(float *mass, const float *q, const float *lse, const 
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.decay = decay;
     p.errors = dev->errors;
-    // Up to 8 warps: the heads in the fewest even passes, the tokens split over what is left.
-    const int passes = (n_kv_heads + kMassMaxWarps - 1) / kMassMaxWarps;
+    // Up to 8 warps: the heads in the fewest even passes (a pass holds the query rows of its
+    // heads, at most 256 of them, in shared memory), the tokens split over the warps left.
+    p.quads = (p.R + 3) / 4;
+    int most = 256 / (4 * p.quads);
+    most = most > kMassMaxWarps ? kMassMaxWarps : (most < 1 ? 1 : most);
+    const int passes = (n_kv_heads + most - 1) / most;
     p.heads_pass = (n_kv_heads + passes - 1) / passes;
     p.subs = kMassMaxWarps / p.heads_pass;
     const int warps = p.heads_pass * p.subs;
-    // query rows held at once: 4, 8 or 16 per KV head (more rows take K again, from L2)
-    if (R <= 4)
+    // up to 8 query rows per KV head stay in registers; more are read back per tile
+    if (p.quads == 1)
         return launch_mass<1>(p, dev, warps, stream);
-    if (R <= 8)
+    if (p.quads == 2)
         return launch_mass<2>(p, dev, warps, stream);
-    return launch_mass<4>(p, dev, warps, stream);
+    return launch_mass<0>(p, dev, warps, stream);
 }
 
 } // extern "C"

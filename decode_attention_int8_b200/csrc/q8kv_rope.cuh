@@ -13,10 +13,11 @@
 //
 // What bounds it: HBM. A token reads (Hq + 2 Hk) D elements and writes 4 Hq D + 2 Hk (D + 4)
 // bytes; a separate rotation would write and read the keys once more. A block takes a tile of
-// up to 4 tokens: it first gathers the tile's cosines and sines into shared memory (one thread
-// per pair, whatever its axis), then its warps stream the tile's rows, 4 (or 2) rows of 8 (16)
-// lanes at once as in the cache write, each warp with the next rows in flight. Neighbouring
-// warps take neighbouring rows, so the block reads and writes contiguous memory. (A first
+// up to 4 tokens: the tile's cosines and sines are gathered into shared memory (one thread per
+// pair, whatever its axis; positions two tiles ahead, table entries one tile ahead by cp.async),
+// and its warps stream the tile's rows, 4 (or 2) rows of 8 (16) lanes at once as in the cache
+// write, each warp with the next rows in flight. Neighbouring warps take neighbouring rows,
+// so the block reads and writes contiguous memory. (A first
 // version gave a warp one token and kept its angles in registers: 24 warps per SM at distant
 // addresses, waiting on every token's position -> table chain, ran the 32768-token fp32 prompt
 // in 632 us.) Few tokens leave SMs empty, so a tile's rows are then split over several blocks.
@@ -199,6 +200,12 @@ __host__ __device__ constexpr int rope_iters(int Hq, int Hk, int D)
 
 constexpr int kRopeTile = 4; // tokens per block and step, at most
 
+// A block's share of one step: a tile of tokens, or a part of its iterations.
+struct RopeUnit {
+    long long tok0;
+    int nt, j, j1; // tokens; this warp's first iteration and the end of the block's
+};
+
 template <int D, typename T, int MODE>
 __global__ void __launch_bounds__(kWriteThreads, 3)
     rope_cache_write_kernel(const __grid_constant__ RopeParams p)
@@ -206,8 +213,8 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
     constexpr int LPR = write_lanes_per_row(D);
     constexpr int PPW = write_pairs_per_warp(D);
     constexpr int C = RowFrag<D>::C;
-    __shared__ __align__(16) float angle[kRopeTile][D]; // cosines, then sines, of a token
-    __shared__ long long tile_slot[kRopeTile];
+    __shared__ __align__(16) float angle[2][kRopeTile][D]; // cosines, then sines, of a token
+    __shared__ long long tile_slot[2][kRopeTile];
     // the new rows may come from the kernel before this one on the stream
     grid_dep_wait();
     grid_dep_launch();
@@ -219,6 +226,17 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
     const long long units = (p.n_tokens + p.tile - 1) / p.tile * p.parts;
     unsigned err = 0;
 
+    auto unit_at = [&](long long unit) {
+        RopeUnit u;
+        const long long tile = unit / p.parts;
+        const int part = (int)(unit - tile * p.parts);
+        u.tok0 = tile * p.tile;
+        u.nt = p.n_tokens - u.tok0 < p.tile ? (int)(p.n_tokens - u.tok0) : p.tile;
+        const int all = u.nt * iters; // iterations of the tile, token by token
+        u.j = part * all / p.parts + warp;
+        u.j1 = (part + 1) * all / p.parts;
+        return u;
+    };
     // this lane's row of iteration it of token `tok`: where it starts, whether it exists
     auto row_of = [&](long long tok, int it, bool &exists, bool &turn) -> const T * {
         if (it < q_iters) {
@@ -235,58 +253,109 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
         return static_cast<const T *>(turn ? p.k_new : p.v_new) + tok * p.kv_stride +
                (long long)h * D;
     };
-
-#pragma unroll 1
-    for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const long long tok0 = unit / p.parts * p.tile;
-        const int part = (int)(unit % p.parts);
-        const int nt = p.n_tokens - tok0 < p.tile ? (int)(p.n_tokens - tok0) : p.tile;
-        const int all = nt * iters; // iterations of the tile, token by token
-        int j = part * all / p.parts + warp;
-        const int j1 = (part + 1) * all / p.parts;
-        int tk = j / iters, it = j - tk * iters;
-        bool exists = false, turn = false;
-        RopeRow<D, T, MODE> cur;
-        if (j < j1) // in flight while the angles are gathered
-            cur = load_row<D, T, MODE>(row_of(tok0 + tk, it, exists, turn), sub, p.rot, turn);
-        for (int t = 0; t < nt; ++t) {
+    // Positions of a unit's tokens for this thread's pair, and (one thread per token) the slot:
+    // loaded two units ahead; the table's entries follow one unit ahead by cp.async.
+    int pos[kRopeTile];
+    long long slot = -1;
+    const int st = tid - (kWriteThreads - kRopeTile); // the token whose slot this thread takes
+    const int axis = tid < half ? p.axis[tid] : 0;
+    auto load_pos = [&](long long unit) {
+        if (unit >= units)
+            return;
+        const RopeUnit u = unit_at(unit);
+#pragma unroll
+        for (int t = 0; t < kRopeTile; ++t)
+            pos[t] = tid < half && t < u.nt ? __ldg(p.pos + axis * p.n_tokens + u.tok0 + t) : 0;
+        if (st >= 0 && st < u.nt)
+            slot = __ldg(p.slots + u.tok0 + st);
+    };
+    auto load_angles = [&](long long unit, int buf) {
+        if (unit < units) {
+            const int nt = unit_at(unit).nt;
             if (tid < half) {
-                int x = __ldg(p.pos + (long long)p.axis[tid] * p.n_tokens + tok0 + t);
-                if (x < 0 || x >= p.max_pos) {
-                    err |= kErrPosition;
-                    x = x < 0 ? 0 : p.max_pos - 1;
+                const uint32_t dst = smem_addr(&angle[buf][0][tid]);
+#pragma unroll
+                for (int t = 0; t < kRopeTile; ++t)
+                    if (t < nt) {
+                        int x = pos[t];
+                        if (x < 0 || x >= p.max_pos) {
+                            err |= kErrPosition;
+                            x = x < 0 ? 0 : p.max_pos - 1;
+                        }
+                        const float *row = p.table + (long long)x * p.rot + tid;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                         dst + (uint32_t)(t * D * 4)),
+                                     "l"(row)
+                                     : "memory");
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                         dst + (uint32_t)((t * D + half) * 4)),
+                                     "l"(row + half)
+                                     : "memory");
+                    }
+            }
+            if (st >= 0 && st < nt) {
+                if (slot >= p.n_slots) {
+                    err |= kErrSlot;
+                    slot = -1;
                 }
-                const float *row = p.table + (long long)x * p.rot + tid;
-                angle[t][tid] = __ldg(row);
-                angle[t][half + tid] = __ldg(row + half);
+                tile_slot[buf][st] = slot;
             }
         }
-        if (tid >= kWriteThreads - kRopeTile && tid - (kWriteThreads - kRopeTile) < nt) {
-            const int t = tid - (kWriteThreads - kRopeTile);
-            long long slot = __ldg(p.slots + tok0 + t);
-            if (slot >= p.n_slots) {
-                err |= kErrSlot;
-                slot = -1;
-            }
-            tile_slot[t] = slot;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    long long unit = blockIdx.x;
+    if (unit >= units)
+        return;
+    RopeUnit u = unit_at(unit);
+    bool exists = false, turn = false;
+    RopeRow<D, T, MODE> cur;
+    int tk = u.j / iters, it = u.j - tk * iters;
+    if (u.j < u.j1)
+        cur = load_row<D, T, MODE>(row_of(u.tok0 + tk, it, exists, turn), sub, p.rot, turn);
+    load_pos(unit);
+    load_angles(unit, 0);
+    load_pos(unit + gridDim.x);
+    for (int buf = 0;; buf ^= 1) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads(); // this unit's angles are there, the last unit's are read no more
+        const long long next_unit = unit + gridDim.x;
+        load_angles(next_unit, buf ^ 1);
+        load_pos(next_unit + gridDim.x);
+        const bool more = next_unit < units;
+        const RopeUnit nu = more ? unit_at(next_unit) : u;
+        bool any = u.j < u.j1;
+        if (!any && more && nu.j < nu.j1) { // nothing to do here: on to the next unit's rows
+            tk = nu.j / iters;
+            it = nu.j - tk * iters;
+            cur = load_row<D, T, MODE>(row_of(nu.tok0 + tk, it, exists, turn), sub, p.rot, turn);
         }
-        __syncthreads();
-#pragma unroll 1
-        for (; j < j1; j += kWriteWarps) {
-            // the next rows are in flight while this iteration's are turned and stored
-            const long long tok = tok0 + tk;
+        while (any) {
+            // the next rows (the next unit's first, at the end) are in flight while this
+            // iteration's are turned and stored
+            const long long tok = u.tok0 + tk;
             const int t = tk, i = it;
+            u.j += kWriteWarps;
             it += kWriteWarps;
             while (it >= iters) {
                 it -= iters;
                 ++tk;
             }
+            any = u.j < u.j1;
+            long long ntok = u.tok0 + tk;
+            bool load = any;
+            if (!any && more && nu.j < nu.j1) {
+                tk = nu.j / iters;
+                it = nu.j - tk * iters;
+                ntok = nu.tok0 + tk;
+                load = true;
+            }
             bool next_exists = false, next_turn = false;
             RopeRow<D, T, MODE> next = cur;
-            if (j + kWriteWarps < j1)
-                next = load_row<D, T, MODE>(row_of(tok0 + tk, it, next_exists, next_turn), sub,
-                                            p.rot, next_turn);
-            const RowFrag<D> f = rotate<D, T, MODE>(cur, angle[t], sub, p.rot, turn);
+            if (load)
+                next = load_row<D, T, MODE>(row_of(ntok, it, next_exists, next_turn), sub, p.rot,
+                                            next_turn);
+            const RowFrag<D> f = rotate<D, T, MODE>(cur, angle[buf][t], sub, p.rot, turn);
             if (i < q_iters) {
                 if constexpr (MODE == kRopeHalf)
                     __syncwarp(); // in place: every lane has read its partners
@@ -299,9 +368,9 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
                 }
             } else {
                 const int r = (i - q_iters) * PPW + grp;
-                const long long slot = tile_slot[t];
-                const bool store = exists && slot >= 0;
-                const long long row = store ? slot * p.Hk + (turn ? r : r - p.Hk) : 0;
+                const long long sl = tile_slot[buf][t];
+                const bool store = exists && sl >= 0;
+                const long long row = store ? sl * p.Hk + (turn ? r : r - p.Hk) : 0;
                 bool bad;
                 const float sc =
                     quantise_row<D>(f, (turn ? p.k : p.v) + row * D, store, sub, bad);
@@ -316,7 +385,10 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
             exists = next_exists;
             turn = next_turn;
         }
-        __syncthreads(); // the angles are written again
+        if (!more)
+            break;
+        unit = next_unit;
+        u = nu;
     }
     if (err)
         atomicOr(p.errors, err);

@@ -160,62 +160,87 @@ __device__ __forceinline__ double piece_sum(const T *pr, const T *qr, int mode, 
     return piece_sum_mode<T, VEC, kWithout>(pr, qr, without, lo, hi, lane);
 }
 
-// The token of piece [lo, hi): the first whose running sum, counted from `base`, exceeds
-// `goal`, or the last of any weight when rounding leaves none. Each lane sums a contiguous
-// part; the part that crosses the goal is divided in the same way, down to one token.
+// The token of piece [lo, hi) (at most kVerifyFind): the first whose running sum, counted from
+// `base`, exceeds `goal`, or the last of any weight when rounding leaves none. One warp: the
+// weights pass through shared memory, so the loads are coalesced and each lane still adds up
+// consecutive tokens; then the lanes' sums are scanned, and the one that crosses the goal
+// walks its tokens.
+constexpr int kVerifyFind = 512;
+
 template <typename T, int MODE>
-__device__ int piece_find_mode(const T *pr, const T *qr, int without, int lo, int hi, double base,
-                               double goal, int lane)
+__device__ __forceinline__ int piece_find_mode(const T *pr, const T *qr, int without, int lo, int hi,
+                                               double base, double goal, int lane, double *sm)
 {
-#pragma unroll 1
-    for (;;) {
-        const int part = (hi - lo + 31) / 32;
-        const int a = lo + lane * part < hi ? lo + lane * part : hi;
-        const int b = a + part < hi ? a + part : hi;
-        double s = 0.0;
-        constexpr int U = 16;
-#pragma unroll 1
-        for (int e = a; e < b; e += U) {
-            float x[U], y[U];
+    constexpr int N = kVerifyFind / 32;
+    float x[N], y[N];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[u] = y[u] = 0.f;
-                if (e + u < b) {
-                    x[u] = as_f32(pr[e + u]);
-                    if constexpr (MODE == kResidual)
-                        y[u] = as_f32(qr[e + u]);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                s += weight<MODE>(x[u], y[u], e + u, without);
+    for (int i = 0; i < N; ++i) {
+        const int e = lo + i * 32 + lane;
+        x[i] = y[i] = 0.f;
+        if (e < hi) {
+            x[i] = as_f32(pr[e]);
+            if constexpr (MODE == kResidual)
+                y[i] = as_f32(qr[e]);
         }
-        const double incl = base + warp_scan(s, lane);
-        unsigned at = __ballot_sync(0xffffffffu, incl > goal && s > 0.0);
-        int sel;
-        if (at) {
-            sel = __ffs(at) - 1;
-        } else { // rounding: the last part of any weight
-            at = __ballot_sync(0xffffffffu, s > 0.0);
-            sel = at ? 31 - __clz(at) : 0;
-        }
-        base = __shfl_sync(0xffffffffu, incl - s, sel);
-        lo = __shfl_sync(0xffffffffu, a, sel);
-        hi = __shfl_sync(0xffffffffu, b, sel);
-        if (part <= 1)
-            return lo;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) { // token k at k + k / N: lanes read without bank conflicts
+        const int k = i * 32 + lane;
+        sm[k + k / N] = weight<MODE>(x[i], y[i], lo + k, without);
+    }
+    __syncwarp();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        s += sm[lane * (N + 1) + i];
+    const double incl = base + warp_scan(s, lane);
+    const unsigned over = __ballot_sync(0xffffffffu, incl > goal && s > 0.0);
+    const unsigned any = __ballot_sync(0xffffffffu, s > 0.0);
+    const int sel = over ? __ffs(over) - 1 : (any ? 31 - __clz(any) : 0);
+    int at = lo + sel * N;
+    if (lane == sel) {
+        double run = incl - s;
+        bool found = false;
+        for (int i = 0; i < N; ++i) {
+            const double w = sm[lane * (N + 1) + i];
+            run += w;
+            if (w > 0.0 && !found) {
+                at = lo + sel * N + i;
+                found = run > goal;
+            }
+        }
+    }
+    return __shfl_sync(0xffffffffu, at, sel);
 }
 
 template <typename T>
 __device__ __forceinline__ int piece_find(const T *pr, const T *qr, int mode, int without, int lo,
-                                          int hi, double base, double goal, int lane)
+                                          int hi, double base, double goal, int lane, double *sm)
 {
     if (mode == kResidual)
-        return piece_find_mode<T, kResidual>(pr, qr, without, lo, hi, base, goal, lane);
+        return piece_find_mode<T, kResidual>(pr, qr, without, lo, hi, base, goal, lane, sm);
     if (mode == kPlain)
-        return piece_find_mode<T, kPlain>(pr, qr, without, lo, hi, base, goal, lane);
-    return piece_find_mode<T, kWithout>(pr, qr, without, lo, hi, base, goal, lane);
+        return piece_find_mode<T, kPlain>(pr, qr, without, lo, hi, base, goal, lane, sm);
+    return piece_find_mode<T, kWithout>(pr, qr, without, lo, hi, base, goal, lane, sm);
+}
+
+// Of consecutive pieces with these sums, the first whose running sum (from `base`, which moves to
+// the piece's start) exceeds `goal`, or the last of any weight.
+__device__ __forceinline__ int crossing(const double *sums, int n, double &base, double goal)
+{
+    double run = base, last_base = base;
+    int last = 0;
+    for (int i = 0; i < n; ++i) {
+        if (sums[i] > 0.0) {
+            last = i;
+            last_base = run;
+            if (run + sums[i] > goal)
+                break;
+        }
+        run += sums[i];
+    }
+    base = last_base;
+    return last;
 }
 
 template <typename T, int VEC>
@@ -226,6 +251,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4)
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ double piece[kVerifyWarps]; // sums of this block's warps
     __shared__ double total[2];            // this block's sum (read by the cluster), by attempt
+    __shared__ double find[kVerifyFind + 32];
     __shared__ int first_refused, count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -352,44 +378,41 @@ __global__ void __launch_bounds__(kVerifyThreads, 4)
             if (i != at)
                 tokens[i] = i < at ? __ldg(drafted + i) : -1;
     }
-    if (rank != owner || warp != 0)
+    if (rank != owner)
         return;
     if (!(Z > 0.0 && Z < INFINITY)) { // nothing to draw from
-        if (lane == 0) {
+        if (tid == 0) {
             tokens[at] = -1;
             atomicOr(p.errors, kErrProbs);
         }
         return;
     }
-    // the warp piece of this block that crosses the goal
-    double run = before, from = before;
-    int sel = -1, lastw = 0;
-    double lastfrom = before;
+    // ---- the warp piece of this block that crosses the goal, divided among the block's warps
+    // until one warp can finish it (every thread follows the same choice)
+    double base = before;
+    int sel = rank * kVerifyWarps + crossing(piece, kVerifyWarps, base, goal);
+    int a = (int)((long long)units * sel / pieces) * kUnit;
+    int z = (int)((long long)units * (sel + 1) / pieces) * kUnit;
+    z = z < p.vocab ? z : p.vocab;
 #pragma unroll 1
-    for (int i = 0; i < kVerifyWarps; ++i) {
-        const double x = piece[i];
-        if (x > 0.0) {
-            lastw = i;
-            lastfrom = run;
-            if (sel < 0 && run + x > goal) {
-                sel = i;
-                from = run;
-            }
-        }
-        run += x;
+    while (z - a > kVerifyFind) {
+        const int per = ((z - a + kVerifyWarps * kUnit - 1) / (kVerifyWarps * kUnit)) * kUnit;
+        const int l = a + warp * per < z ? a + warp * per : z;
+        const int h = l + per < z ? l + per : z;
+        __syncthreads(); // piece[] has been read
+        const double s = piece_sum<T, VEC>(pr, qr, mode, without, l, h, lane);
+        if (lane == 0)
+            piece[warp] = s;
+        __syncthreads();
+        sel = crossing(piece, kVerifyWarps, base, goal);
+        a = a + sel * per;
+        z = a + per < z ? a + per : z;
     }
-    if (sel < 0) {
-        sel = lastw;
-        from = lastfrom;
+    if (warp == 0) {
+        const int x = piece_find<T>(pr, qr, mode, without, a, z, base, goal, lane, find);
+        if (lane == 0)
+            tokens[at] = x;
     }
-    const int sw = rank * kVerifyWarps + sel;
-    const int su0 = (int)((long long)units * sw / pieces);
-    const int su1 = (int)((long long)units * (sw + 1) / pieces);
-    const int slo = su0 * kUnit < p.vocab ? su0 * kUnit : p.vocab;
-    const int shi = su1 * kUnit < p.vocab ? su1 * kUnit : p.vocab;
-    const int x = piece_find<T>(pr, qr, mode, without, slo, shi, from, goal, lane);
-    if (lane == 0)
-        tokens[at] = x;
 }
 
 } // namespace q8kv
