@@ -7,26 +7,28 @@
 // with the decode's own scores s (int8 query blocks, exact block dots, q8kv_decode.cuh) and
 // the log-sum-exp of each row that the decode left: one pass over K, no softmax to redo.
 //
-// What bounds it: HBM, at 132 bytes of K and 8 of mass per (token, KV head). A warp takes 16
-// tokens of one head at a time: tokens are the M rows of mma.m16n8k32.s8, four query rows its N
-// columns twice over. A lane owns 16 consecutive bytes of a token's row; with those as the MMA's
-// k positions, lanes c = 0, 1 hold block 2h of the row (h: which half) and lanes c = 2, 3 block
-// 2h + 1, and the query operand is zero where column group n / 4 and block differ. One
-// accumulator so carries two blocks' exact dots side by side, every column is used, and two
-// shuffles bring the halves together, each lane keeping two rows of one token.
+// What bounds it: HBM, at 132 bytes of K and 8 of mass per (token, KV head), then the issue
+// slots. A warp takes 16 tokens of one head at a time as the M rows of mma.m16n8k32.s8, query
+// rows as its N columns:
+//  * 5 or more rows per head: eight rows per MMA, one MMA per 32-channel block, K fragments by
+//    ldmatrix.
+//  * up to 4 rows (they would leave half the columns empty): four rows twice over. A lane takes
+//    16 consecutive bytes of a token's row as its k positions, so lanes c = 0, 1 hold block 2h
+//    of the row (h: which half) and lanes c = 2, 3 block 2h + 1; the query operand is zero where
+//    column group n / 4 and block differ. One accumulator so carries two blocks' exact dots
+//    side by side, and two shuffles bring the halves together, each lane keeping one token.
 //
-// Every lane copies its own bytes (and its token's scale and old mass) ahead of use with
-// cp.async into a ring of kMassStages tiles in shared memory that only it reads: the copies in
-// flight cost no registers and no synchronisation. (With the next tile's operands in registers
-// instead, the kernel spilled at 24 warps per SM and took 114 us on 48 ragged sequences of up
-// to 16384 tokens, 64 / 8 heads; at 16 warps 107 us.) The tokens of all sequences form one list
-// that the blocks share evenly; a block's warps take different heads of the same tokens,
-// whose rows are neighbours in the pool. The block quantises a segment's query rows together,
-// into shared memory, while the first tiles are on their way.
+// A warp copies its tiles (rows, scales, old masses) ahead of use with cp.async into a ring of
+// kMassStages tiles in shared memory that only it reads: the copies in flight cost no registers
+// and no block-wide synchronisation. (With the next tile's operands in registers instead, the
+// kernel spilled at 24 warps per SM and took 114 us on 48 ragged sequences of up to 16384
+// tokens, 64 / 8 heads.) The tokens of all sequences form one list that the blocks share
+// evenly; a block's warps take different heads of the same tokens, whose rows are neighbours
+// in the pool. The block quantises a segment's query rows together, into shared memory, while
+// the first tiles are on their way.
 #pragma once
 
 #include <cstdint>
-#include <type_traits>
 
 #include "q8kv_decode.cuh"
 
@@ -36,8 +38,13 @@ constexpr int kMassMaxWarps = 8;
 constexpr int kMassTile = 16;    // tokens per warp step
 constexpr int kMassStages = 4;   // tiles in a warp's ring
 constexpr int kMassMaxBatch = 16384;
+// A block that goes on to another sequence drains its rings, quantises the new query and fills
+// them again, in about the time of this many of its tiles; the even split of the list counts
+// them at every sequence's start. (48 ragged sequences, 64 / 8 heads: 79.6 us without.)
+constexpr int kMassStartTiles = 6;
 constexpr int kMassMaxRows = 128; // query rows per KV head
-constexpr int kMassStageBytes = 32 * (64 + 8); // per lane: 64 bytes of K, the scale, the mass
+constexpr int kMassStageBytes = kMassTile * (kD + 8); // rows, then scales, then masses
+constexpr int kMassRowBytes = kD + 16; // a query row in shared memory (rows on distinct banks)
 
 struct MassParams {
     float *mass;       // [B][Hk][cap]
@@ -47,7 +54,7 @@ struct MassParams {
     const float *ks;
     const int32_t *table, *lens;
     int B, nq, Hq, Hk, Gq, R; // Gq: query heads per KV head; R = nq Gq rows per KV head
-    int quads;         // R / 4, rounded up
+    int rows;          // R rounded up to 4 (one quad) or to a multiple of 8
     int bs_log2, mbps, num_blocks, cap;
     int heads_pass;    // heads the block's warps cover at once
     int subs;          // warps that share a head's tokens
@@ -60,45 +67,58 @@ struct MassLayout {
     uint32_t off_codes, off_zero, off_qs, off_lse, off_view, off_prefix, total;
 };
 
-__host__ __device__ inline MassLayout mass_layout(int warps, int heads, int quads, int B)
+__host__ __device__ inline MassLayout mass_layout(int warps, int heads, int rows, int B)
 {
     MassLayout l;
     uint32_t o = (uint32_t)(warps * kMassStages * kMassStageBytes);
-    l.off_codes = o; // [head][row][128]
-    o += (uint32_t)(heads * quads * 4 * kD);
+    l.off_codes = o; // [head][row]
+    o += (uint32_t)(heads * rows * kMassRowBytes);
     l.off_zero = o;  // 128 bytes of zeros
     o += kD;
-    l.off_qs = o;    // [head][quad][c][half][row]: scales in the order the lanes use them
-    o += (uint32_t)(heads * quads * 16 * 4);
+    l.off_qs = o;    // scales in the order the lanes use them: a quad's [c][half][row], a
+                     // group of eight's [c][block][row]
+    o += (uint32_t)(heads * rows * kNB * 4);
     l.off_lse = o;   // [head][row]: log-sum-exp, base 2 (+inf: no row)
-    o += (uint32_t)(heads * quads * 4 * 4);
+    o += (uint32_t)(heads * rows * 4);
     l.off_view = o;  // [row]: index of the row's query token
-    o += (uint32_t)(quads * 4 * 4);
+    o += (uint32_t)(rows * 4);
     l.off_prefix = o;
     l.total = o + 4u * (uint32_t)(B + 1);
     return l;
 }
 
-// The query operand of four rows in the lane order described above, with the scales and
-// log-sum-exp of the two rows whose scores this lane keeps.
-struct MassQuad {
-    uint4 b[2];      // [half]: the lane's 16 code bytes
-    float qs[2][2];  // [half][row]: scale of the lane's block
+// Operand of four rows (kMassQuad): the lane's bytes, or zeros; of eight rows: column g's
+// words. With the scales of the rows whose dots this lane holds, and their log-sum-exp.
+struct MassOperand {
+    uint32_t b[8];
+    float qs[8]; // (a quad's: the first four)
     float lse2[2];
 };
+
+enum MassMode { kMassQuad = 0, kMassOct = 1, kMassOcts = 2 };
 
 __device__ __forceinline__ void mass_cp16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ void mass_cp4(uint32_t dst, const void *src)
+__device__ __forceinline__ void mass_cp4(uint32_t dst, const void *src, uint32_t bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
 }
 
-// NQ: quads held in registers (all of a head's rows), 0: read from shared memory per tile.
-template <int NQ>
+__device__ __forceinline__ void mass_ldsm_x4(uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3,
+                                        uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr));
+}
+
+// MODE: kMassQuad for up to 4 rows per head, kMassOct for up to 8 (both held in registers),
+// kMassOcts for more (read from shared memory per tile).
+template <int MODE>
 __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
     attn_mass_kernel(const __grid_constant__ MassParams p)
 {
@@ -107,16 +127,17 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nwarps = blockDim.x >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const MassLayout lay = mass_layout(nwarps, p.heads_pass, p.quads, p.B);
-    int *prefix = reinterpret_cast<int *>(msm + lay.off_prefix); // tiles before each sequence
+    const MassLayout lay = mass_layout(nwarps, p.heads_pass, p.rows, p.B);
+    int *prefix = reinterpret_cast<int *>(msm + lay.off_prefix); // units before each sequence
     // the query, its statistics and the cache come from kernels before this one
     grid_dep_wait();
     grid_dep_launch();
 
-    // ---- tiles of every sequence, as prefix sums; the rows' query indices
+    // ---- units of every sequence (its tiles and the charge for its start), as prefix sums; the
+    // rows' query indices
     if (tid < kD / 4)
         reinterpret_cast<uint32_t *>(msm + lay.off_zero)[tid] = 0u;
-    for (int r = tid; r < 4 * p.quads; r += blockDim.x)
+    for (int r = tid; r < p.rows; r += blockDim.x)
         reinterpret_cast<int *>(msm + lay.off_view)[r] = r / p.Gq;
     int carry = 0;
 #pragma unroll 1
@@ -129,7 +150,7 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
                 atomicOr(p.errors, kErrSeqLen);
                 L = L < 0 ? 0 : p.cap;
             }
-            n = (L + kMassTile - 1) / kMassTile;
+            n = L > 0 ? (L + kMassTile - 1) / kMassTile + kMassStartTiles : 0;
         }
         int v = n;
 #pragma unroll
@@ -155,33 +176,46 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
         prefix[0] = 0;
     __syncthreads();
     const int N = carry;
-    int t0 = (int)((long long)N * blockIdx.x / gridDim.x);
-    const int t1 = (int)((long long)N * (blockIdx.x + 1) / gridDim.x);
+    int u0 = (int)((long long)N * blockIdx.x / gridDim.x);
+    const int u1 = (int)((long long)N * (blockIdx.x + 1) / gridDim.x);
     const int hw = warp % p.heads_pass, sub = warp / p.heads_pass;
-    const int bs_mask = (1 << p.bs_log2) - 1;
-    const int sel = c >> 1; // which half of the tile's tokens this lane keeps
-    const bool writer = (c & 1) == 0;
-    const unsigned row8 = 8u * (unsigned)p.Hk * kD; // bytes from token t's row to t + 8's
+    const unsigned bs_mask = (1u << p.bs_log2) - 1u;
+    const int sel = c >> 1; // which half of the tile's tokens this lane ends up with
     const bool old = p.decay != 0.f;
-    // this lane's part of the ring: 16-byte slots 512 bytes apart, then the 4-byte ones
-    const uint32_t ring = smem_addr(msm) + (uint32_t)(warp * kMassStages * kMassStageBytes);
-    const uint32_t mine16 = ring + 16u * lane, mine4 = ring + 2048u + 4u * lane;
-    // this lane's query bytes of a quad: those of row g & 3 where its block is in column group
-    // g / 4, else zeros
-    const bool in_col = (c >> 1) == (g >> 2);
+    const unsigned hkd = (unsigned)p.Hk * kD; // bytes from token to token
+    const unsigned long long row8 = 8ull * hkd;
+    const unsigned long long kstep = (unsigned long long)(p.subs * kMassTile) * hkd;
+    const uint32_t bytes4 = lane < 16 || old ? 4u : 0u; // (0: filled with zeros, nothing read)
 
-    while (t0 < t1) {
-        // the sequence of tile t0: the last b with prefix[b] <= t0
+    // The warp's ring. Copies: lane (g, c) moves 16-byte chunks c and c + 4 of rows g and g + 8,
+    // to chunk positions XORed with the row (ldmatrix then meets every bank once; a lane that
+    // reads its own chunks back finds them where it put them); lanes 0-15 move the tokens'
+    // scales, lanes 16-31 their masses.
+    const uint32_t ring = smem_addr(msm) + (uint32_t)(warp * kMassStages * kMassStageBytes);
+    const uint32_t put_row = ring + (uint32_t)(g * kD);
+    const uint32_t put0 = put_row + (uint32_t)((c ^ g) * 16), put1 = put_row + (uint32_t)(((c + 4) ^ g) * 16);
+    const uint32_t put_s = ring + (uint32_t)(kMassTile * kD + 4 * lane);
+    const uint32_t get_s = ring + (uint32_t)(kMassTile * kD + 4 * g);
+    // ldmatrix addresses: lanes 0-7 rows 0-7, 8-15 rows 8-15 of a block's first 16 bytes, lanes
+    // 16-31 the same of its last 16
+    const uint32_t get_m = ring + (uint32_t)((lane & 15) * kD);
+    const int get_c = (lane >> 4) ^ (lane & 7); // chunk 2j + lane / 16, XORed with the row
+
+    while (u0 < u1) {
+        // the sequence of unit u0: the last b with prefix[b] <= u0
         int b = 0, z = p.B - 1;
         while (b < z) {
             const int m = (b + z + 1) >> 1;
-            if (prefix[m] <= t0)
+            if (prefix[m] <= u0)
                 b = m;
             else
                 z = m - 1;
         }
-        const int first = prefix[b];
-        const int t2 = min(t1, prefix[b + 1]);
+        const int first = prefix[b] + kMassStartTiles, end = prefix[b + 1];
+        const int t0 = max(u0 - first, 0), t2 = min(u1, end) - first; // the block's tiles of it
+        u0 = min(u1, end);
+        if (t0 >= t2)
+            continue;
         int L = __ldg(p.lens + b);
         L = L > p.cap ? p.cap : L;
         const int32_t *table = p.table + (long long)b * p.mbps;
@@ -189,58 +223,68 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
 #pragma unroll 1
         for (int kv0 = 0; kv0 < p.Hk; kv0 += p.heads_pass) {
             const int kv = kv0 + hw;
-            float *mass = p.mass + ((long long)b * p.Hk + kv) * p.cap + g + 8 * sel;
+            float *mass_row = p.mass + ((long long)b * p.Hk + kv) * p.cap;
+            float *mass = mass_row + g + 8 * sel;
             const int8_t *kbase = p.k + ((long long)g * p.Hk + kv) * kD + 16 * c;
-            const float *sbase = p.ks + (long long)(g + 8 * sel) * p.Hk + kv;
+            // this lane's 4-byte copy: a scale (by slot) or a mass (by position)
+            const float *base4 = lane < 16 ? p.ks + (long long)lane * p.Hk + kv
+                                           : mass_row + (lane - 16);
+            const unsigned stride4 = lane < 16 ? (unsigned)p.Hk * 4u : 4u;
+            const unsigned step4 = (unsigned)(p.subs * kMassTile) * stride4;
             const int step = p.subs * kMassTile;
-            const int tok1 = kv < p.Hk ? (t2 - first) * kMassTile : 0;
-            int ti = (t0 - first + sub) * kMassTile; // first token of the next tile to fetch
+            const int tok1 = kv < p.Hk ? t2 * kMassTile : 0;
+            int t = (t0 + sub) * kMassTile; // first token of the tile in use
+            // Tiles are fetched in order; within one block of the table the addresses only
+            // advance, so the table and the products are left to the step into a new one.
+            int ti = t;             // first token of the next tile to fetch
+            int left = 0;           // tiles of its block still to fetch
+            const int8_t *kp = kbase;
+            const char *p4 = reinterpret_cast<const char *>(base4);
+            unsigned ok = 0;        // the block is in the pool
+            uint32_t usable = 0;    // `ok` of the fetched tiles, latest lowest
             int blk = ti < tok1 ? __ldg(table + (ti >> p.bs_log2)) : 0;
-            uint32_t usable = 0;                     // one bit per fetched tile, latest lowest
-            uint32_t put = 0;                        // ring offset of the next tile
-            auto fetch = [&]() {
-                usable <<= 1;
+            auto fetch = [&](uint32_t put) {
                 if (ti < tok1) {
-                    const bool ok = (unsigned)blk < (unsigned)p.num_blocks;
-                    if (ok) {
-                        const int slot = (blk << p.bs_log2) + (ti & bs_mask);
-                        const long long row = (long long)slot * p.Hk; // (slot, head 0)
-                        const int8_t *k = kbase + row * kD;
-                        mass_cp16(mine16 + put, k);
-                        mass_cp16(mine16 + put + 512, k + 64);
-                        mass_cp16(mine16 + put + 1024, k + row8);
-                        mass_cp16(mine16 + put + 1536, k + row8 + 64);
-                        mass_cp4(mine4 + put, sbase + row);
-                        // (in bounds of the row: a tile never passes the table's last block)
-                        if (old)
-                            mass_cp4(mine4 + put + 128, mass + ti);
-                        usable |= 1u;
-                    } else if (lane == 0) {
-                        atomicOr(p.errors, kErrBlockTable);
+                    if (left == 0) {
+                        ok = (unsigned)blk < (unsigned)p.num_blocks;
+                        const unsigned in = (unsigned)ti & bs_mask;
+                        const unsigned slot = ((ok ? (unsigned)blk : 0u) << p.bs_log2) + in;
+                        left = (int)((bs_mask - in) / (unsigned)step) + 1;
+                        kp = kbase + (unsigned long long)slot * hkd;
+                        p4 = reinterpret_cast<const char *>(base4) +
+                             (unsigned long long)(lane < 16 ? slot : (unsigned)ti) * stride4;
+                        if (!ok && lane == 0)
+                            atomicOr(p.errors, kErrBlockTable);
+                        const int tn = ti + left * step; // the next block, one block ahead
+                        if (tn < tok1)
+                            blk = __ldg(table + (tn >> p.bs_log2));
                     }
+                    mass_cp16(put0 + put, kp);
+                    mass_cp16(put1 + put, kp + 64);
+                    mass_cp16(put0 + put + 8 * kD, kp + row8);
+                    mass_cp16(put1 + put + 8 * kD, kp + row8 + 64);
+                    // (in bounds of the row: a tile never passes the table's last block)
+                    mass_cp4(put_s + put, p4, bytes4);
+                    kp += kstep;
+                    p4 += step4;
                     ti += step;
-                    if (ti < tok1) // (the next tile's block, a step ahead)
-                        blk = __ldg(table + (ti >> p.bs_log2));
+                    --left;
                 }
+                usable = usable * 2u + ok;
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                put = put == (kMassStages - 1) * kMassStageBytes ? 0 : put + kMassStageBytes;
             };
-            int t = ti; // first token of the tile in use
+            // ---- the segment's query rows, by the whole block: 16 lanes per row. The first of
+            // them are loaded before the copies wait for the table, and quantised after.
+            const int part = lane & 15; // block part / 4, its values 8 (part % 4) ..
+            float v[8], l2;
+            auto load_query = [&](int x) {
+                const int hd = MODE == kMassQuad ? x >> 2 : (MODE == kMassOct ? x >> 3 : x / p.rows);
+                const int r = x - hd * p.rows;
+                l2 = INFINITY;
 #pragma unroll
-            for (int i = 0; i < kMassStages - 1; ++i)
-                fetch();
-
-            // ---- the segment's query rows, by the whole block: 16 lanes per row
-            __syncthreads(); // the last segment's rows have been read
-#pragma unroll 1
-            for (int x0 = 2 * warp; x0 < p.heads_pass * 4 * p.quads; x0 += 2 * nwarps) {
-                const int x = x0 + (lane >> 4);
-                const int hd = x / (4 * p.quads), r = x - hd * 4 * p.quads;
-                const int part = lane & 15; // block part / 4, its values 8 (part % 4) ..
-                const bool live = r < p.R && kv0 + hd < p.Hk;
-                float v[8];
-                float l2 = INFINITY;
-                if (live) {
+                for (int i = 0; i < 8; ++i)
+                    v[i] = 0.f;
+                if (r < p.R && hd < p.heads_pass && kv0 + hd < p.Hk) {
                     const int i = reinterpret_cast<const int *>(msm + lay.off_view)[r];
                     const long long row = ((long long)b * p.nq + i) * p.Hq +
                                           (long long)(kv0 + hd) * p.Gq + (r - i * p.Gq);
@@ -250,82 +294,111 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
                     v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
                     v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
                     l2 = __ldg(p.lse + row) * 1.44269504088896341f;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = 0.f;
                 }
+            };
+            load_query(2 * warp + (lane >> 4));
+#pragma unroll
+            for (int i = 0; i < kMassStages - 1; ++i)
+                fetch(i * kMassStageBytes);
+            __syncthreads(); // the last segment's rows have been read
+#pragma unroll 1
+            for (int x0 = 2 * warp; x0 < p.heads_pass * p.rows; x0 += 2 * nwarps) {
+                const int x = x0 + (lane >> 4);
+                const int hd = MODE == kMassQuad ? x >> 2 : (MODE == kMassOct ? x >> 3 : x / p.rows);
+                const int r = x - hd * p.rows;
+                if (x0 != 2 * warp)
+                    load_query(x);
                 uint32_t lo, hi;
                 float qsc;
                 quantize_block_quad(v, lo, hi, qsc);
                 if (hd < p.heads_pass) { // (the last step may pass the last row)
                     *reinterpret_cast<uint2 *>(msm + lay.off_codes +
-                                               (uint32_t)(x * kD + 8 * part)) =
+                                               (uint32_t)(x * kMassRowBytes + 8 * part)) =
                         make_uint2(lo, hi);
                     if ((part & 3) == 0) {
-                        // block j = 2h + c / 2 of row 2 (c & 1) + e lies at [c][h][e]
-                        const int j = part >> 2, rr = r & 3;
-                        const int cc = 2 * (j & 1) + (rr >> 1);
-                        reinterpret_cast<float *>(
-                            msm + lay.off_qs)[((x >> 2) * 4 + cc) * 4 + (j >> 1) * 2 + (rr & 1)] =
-                            qsc;
+                        float *qs = reinterpret_cast<float *>(msm + lay.off_qs);
+                        const int j = part >> 2;
+                        if constexpr (MODE == kMassQuad) {
+                            // block j = 2h + c / 2 of row 2 (c & 1) + e lies at [c][h][e]
+                            const int cc = 2 * (j & 1) + (r >> 1);
+                            qs[(hd * 4 + cc) * 4 + (j >> 1) * 2 + (r & 1)] = qsc;
+                        } else { // row 2c + e of its eight at [c][j][e]
+                            qs[((x >> 3) * 4 + ((r & 7) >> 1)) * 8 + j * 2 + (r & 1)] = qsc;
+                        }
                     }
                     if (part == 0)
                         reinterpret_cast<float *>(msm + lay.off_lse)[x] = l2;
                 }
             }
             __syncthreads();
-            auto quad = [&](int n) {
-                MassQuad q;
-                const int row = (hw * p.quads + n) * 4;
-                const uint8_t *codes = in_col ? msm + lay.off_codes + (row + (g & 3)) * kD
-                                              : msm + lay.off_zero;
-                q.b[0] = *reinterpret_cast<const uint4 *>(codes + 16 * c);
-                q.b[1] = *reinterpret_cast<const uint4 *>(codes + 64 + 16 * c);
-                const float4 s = *reinterpret_cast<const float4 *>(msm + lay.off_qs +
-                                                                   (uint32_t)(row + c) * 16u);
-                q.qs[0][0] = s.x, q.qs[0][1] = s.y, q.qs[1][0] = s.z, q.qs[1][1] = s.w;
-                const float2 l = *reinterpret_cast<const float2 *>(
-                    msm + lay.off_lse + (uint32_t)(row + 2 * (c & 1)) * 4u);
-                q.lse2[0] = l.x, q.lse2[1] = l.y;
+            auto operand = [&](int n) { // quad, or group n of eight, of this warp's head
+                MassOperand q;
+                if constexpr (MODE == kMassQuad) {
+                    const bool in_col = (c >> 1) == (g >> 2);
+                    const uint8_t *codes =
+                        in_col ? msm + lay.off_codes + (hw * 4 + (g & 3)) * kMassRowBytes
+                               : msm + lay.off_zero;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(codes + 16 * c);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(codes + 64 + 16 * c);
+                    q.b[0] = x.x, q.b[1] = x.y, q.b[2] = x.z, q.b[3] = x.w;
+                    q.b[4] = y.x, q.b[5] = y.y, q.b[6] = y.z, q.b[7] = y.w;
+                    const float4 s = *reinterpret_cast<const float4 *>(
+                        msm + lay.off_qs + (uint32_t)(hw * 4 + c) * 16u);
+                    q.qs[0] = s.x, q.qs[1] = s.y, q.qs[2] = s.z, q.qs[3] = s.w;
+                    const float2 l = *reinterpret_cast<const float2 *>(
+                        msm + lay.off_lse + (uint32_t)(hw * 4 + 2 * (c & 1)) * 4u);
+                    q.lse2[0] = l.x, q.lse2[1] = l.y;
+                } else {
+                    const int row = hw * p.rows + 8 * n;
+                    const uint8_t *codes = msm + lay.off_codes + (row + g) * kMassRowBytes + 4 * c;
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j) {
+                        q.b[2 * j] = *reinterpret_cast<const uint32_t *>(codes + 32 * j);
+                        q.b[2 * j + 1] = *reinterpret_cast<const uint32_t *>(codes + 32 * j + 16);
+                    }
+                    const float4 *s = reinterpret_cast<const float4 *>(
+                        msm + lay.off_qs + (uint32_t)((row >> 3) * 4 + c) * 32u);
+                    const float4 s0 = s[0], s1 = s[1];
+                    q.qs[0] = s0.x, q.qs[1] = s0.y, q.qs[2] = s0.z, q.qs[3] = s0.w;
+                    q.qs[4] = s1.x, q.qs[5] = s1.y, q.qs[6] = s1.z, q.qs[7] = s1.w;
+                    const float2 l = *reinterpret_cast<const float2 *>(
+                        msm + lay.off_lse + (uint32_t)(row + 2 * c) * 4u);
+                    q.lse2[0] = l.x, q.lse2[1] = l.y;
+                }
                 return q;
             };
-            MassQuad held[NQ > 0 ? NQ : 1];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-                held[n] = quad(n);
+            MassOperand held;
+            if constexpr (MODE != kMassOcts)
+                held = operand(0);
+            const int *view = reinterpret_cast<const int *>(msm + lay.off_view);
 
             // ---- the tiles
-            uint32_t get = 0;
+            uint32_t at = 0, last = (kMassStages - 1) * kMassStageBytes; // this tile, the one before
+            float *out = mass + t;
 #pragma unroll 1
             for (; t < tok1; t += step) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kMassStages - 2) : "memory");
-                const uint4 x0 = lds128(mine16 + get), x1 = lds128(mine16 + get + 512);
-                const uint4 y0 = lds128(mine16 + get + 1024), y1 = lds128(mine16 + get + 1536);
-                const float ksl = lds_f32(mine4 + get) * p.scale_log2;
-                const float before = old ? lds_f32(mine4 + get + 128) : 0.f;
-                get = get == (kMassStages - 1) * kMassStageBytes ? 0 : get + kMassStageBytes;
-                fetch(); // into the tile consumed last
-                if (!((usable >> (kMassStages - 1)) & 1u))
-                    continue;
+                __syncwarp(); // (and every lane has read the tile that fetch() overwrites)
                 const bool full = t + kMassTile <= all_see; // every row sees all its tokens
-                const int tok = t + g + 8 * sel;
-                // the sum of the two rows' weights of this lane in quad n
-                auto weights = [&](const MassQuad &q, int n) {
+                float w;
+                const float before = lds_f32(get_s + at + 64 + 32 * sel);
+                if constexpr (MODE == kMassQuad) {
+                    const uint4 x0 = lds128(put0 + at), x1 = lds128(put1 + at);
+                    const uint4 y0 = lds128(put0 + at + 8 * kD), y1 = lds128(put1 + at + 8 * kD);
+                    const float ksl = lds_f32(get_s + at + 32 * sel) * p.scale_log2;
+                    fetch(last);
+                    int d[4], f[4];
+                    mma_s8_16832(d, x0.x, y0.x, x0.y, y0.y, held.b[0], held.b[1]);
+                    mma_s8_16832_acc(d, x0.z, y0.z, x0.w, y0.w, held.b[2], held.b[3], d);
+                    mma_s8_16832(f, x1.x, y1.x, x1.y, y1.y, held.b[4], held.b[5]);
+                    mma_s8_16832_acc(f, x1.z, y1.z, x1.w, y1.w, held.b[6], held.b[7], f);
                     float s[2][2]; // [token half][row]
-                    int d[4];
-                    mma_s8_16832_biased(d, x0.x, y0.x, x0.y, y0.y, q.b[0].x, q.b[0].y);
-                    mma_s8_16832_acc(d, x0.z, y0.z, x0.w, y0.w, q.b[0].z, q.b[0].w, d);
-                    int f[4];
-                    mma_s8_16832_biased(f, x1.x, y1.x, x1.y, y1.y, q.b[1].x, q.b[1].y);
-                    mma_s8_16832_acc(f, x1.z, y1.z, x1.w, y1.w, q.b[1].z, q.b[1].w, f);
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) // the biased views minus the bias: exact
-                            s[u][e] = fmaf(__int_as_float(f[2 * u + e]) - kDotBiasF, q.qs[1][e],
-                                           (__int_as_float(d[2 * u + e]) - kDotBiasF) *
-                                               q.qs[0][e]);
+                        for (int e = 0; e < 2; ++e)
+                            s[u][e] = fmaf((float)f[2 * u + e], held.qs[2 + e],
+                                           (float)d[2 * u + e] * held.qs[e]);
                     // blocks 0, 2 lie in lanes c < 2 and blocks 1, 3 in lanes c >= 2 (of the
                     // same rows): each lane gives the token it does not keep
                     float a[2];
@@ -334,33 +407,71 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
                         const float give = sel ? s[0][e] : s[1][e];
                         const float keep = sel ? s[1][e] : s[0][e];
                         const float x = keep + __shfl_xor_sync(kFullMask, give, 2);
-                        a[e] = fast_exp2(fmaf(x, ksl, -q.lse2[e]));
+                        a[e] = fast_exp2(fmaf(x, ksl, -held.lse2[e]));
                     }
                     if (!full) {
-                        const int2 v = *reinterpret_cast<const int2 *>(
-                            msm + lay.off_view + (uint32_t)(4 * n + 2 * (c & 1)) * 4u);
-                        a[0] = tok < all_see + v.x ? a[0] : 0.f;
-                        a[1] = tok < all_see + v.y ? a[1] : 0.f;
-                    }
-                    return a[0] + a[1];
-                };
-                float w = 0.f;
-                if constexpr (NQ > 0) {
+                        const int tok = t + g + 8 * sel;
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-                        w += weights(held[n], n);
+                        for (int e = 0; e < 2; ++e)
+                            a[e] = tok < all_see + view[2 * (c & 1) + e] ? a[e] : 0.f;
+                    }
+                    w = a[0] + a[1];
                 } else {
+                    uint32_t k[kNB][4];
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j)
+                        mass_ldsm_x4(k[j][0], k[j][1], k[j][2], k[j][3],
+                                get_m + at + (uint32_t)((get_c ^ (2 * j)) * 16));
+                    const float ks0 = lds_f32(get_s + at) * p.scale_log2;
+                    const float ks1 = lds_f32(get_s + at + 32) * p.scale_log2;
+                    fetch(last);
+                    float w0 = 0.f, w1 = 0.f;
+                    auto group = [&](const MassOperand &q, int n) {
+                        float s[4];
+#pragma unroll
+                        for (int j = 0; j < kNB; ++j) {
+                            int d[4];
+                            mma_s8_16832(d, k[j][0], k[j][1], k[j][2], k[j][3], q.b[2 * j],
+                                         q.b[2 * j + 1]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                s[i] = j == 0 ? (float)d[i] * q.qs[i & 1]
+                                              : fmaf((float)d[i], q.qs[2 * j + (i & 1)], s[i]);
+                        }
+                        float a[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            a[i] = fast_exp2(fmaf(s[i], i < 2 ? ks0 : ks1, -q.lse2[i & 1]));
+                        if (!full) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                a[i] = t + g + 8 * (i >> 1) <
+                                               all_see + view[8 * n + 2 * c + (i & 1)]
+                                           ? a[i]
+                                           : 0.f;
+                        }
+                        w0 += a[0] + a[1];
+                        w1 += a[2] + a[3];
+                    };
+                    if constexpr (MODE == kMassOct) {
+                        group(held, 0);
+                    } else {
 #pragma unroll 1
-                    for (int n = 0; n < p.quads; ++n)
-                        w += weights(quad(n), n);
+                        for (int n = 0; n < p.rows >> 3; ++n)
+                            group(operand(n), n);
+                    }
+                    w = (sel ? w1 : w0) + __shfl_xor_sync(kFullMask, sel ? w0 : w1, 2);
                 }
                 w += __shfl_xor_sync(kFullMask, w, 1);
-                if (writer && (full || tok < L))
-                    mass[t] = old ? fmaf(p.decay, before, w) : w;
+                if ((c & 1) == 0 && (full || t + g + 8 * sel < L) &&
+                    ((usable >> (kMassStages - 1)) & 1u))
+                    *out = fmaf(p.decay, before, w); // (before is zero without decay)
+                out += step;
+                last = at;
+                at = at == (kMassStages - 1) * kMassStageBytes ? 0 : at + kMassStageBytes;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
-        t0 = t2;
     }
 }
 

@@ -11,26 +11,26 @@ using namespace q8kv;
 
 bool g_mass_attr[kMaxDevices][3];
 
-template <int NQ>
+template <int MODE>
 q8kv_status launch_mass(const MassParams &p, DeviceInfo *dev, int warps, cudaStream_t stream)
 {
-    bool &set = g_mass_attr[dev - g_dev][NQ];
+    bool &set = g_mass_attr[dev - g_dev][MODE];
     {
         std::lock_guard<std::mutex> lock(g_mutex);
         if (!set) {
-            Q8KV_CUDA(cudaFuncSetAttribute(attn_mass_kernel<NQ>,
+            Q8KV_CUDA(cudaFuncSetAttribute(attn_mass_kernel<MODE>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            dev->smem_optin - 1024));
             set = true;
         }
     }
-    const uint32_t smem = mass_layout(warps, p.heads_pass, p.quads, p.B).total;
+    const uint32_t smem = mass_layout(warps, p.heads_pass, p.rows, p.B).total;
     // as many blocks as one wave holds: 3 per SM (24 warps), fewer with many query rows or
     // sequences
     long long wave = (long long)(dev->smem_optin / (smem + 1024));
     wave = (wave < 1 ? 1 : (wave > 3 ? 3 : wave)) * dev->sms;
     const long long tiles = (long long)p.B * ((p.cap + kMassTile - 1) / kMassTile);
-    return launch_pdl(attn_mass_kernel<NQ>, p, (unsigned)(tiles < wave ? tiles : wave),
+    return launch_pdl(attn_mass_kernel<MODE>, p, (unsigned)(tiles < wave ? tiles : wave),
                       (unsigned)warps * 32u, smem, stream);
 }
 
@@ -62,7 +62,7 @@ q8kv_status q8kv_attn_mass(float *mass, const float *q, const float *lse, const 
         R > kMassMaxRows || B > kMassMaxBatch || n_kv_heads > 4096 ||
         (long long)num_kv_blocks * kv_block_size >= (1LL << 31) ||
         (long long)max_blocks_per_seq * kv_block_size >= (1LL << 30) ||
-        (long long)B * max_blocks_per_seq * (kv_block_size / 16) >= (1LL << 31))
+        (long long)B * max_blocks_per_seq * (kv_block_size / 16) >= (1LL << 30))
         return Q8KV_ERR_UNSUPPORTED;
     DeviceInfo *dev = nullptr;
     q8kv_status st;
@@ -95,19 +95,18 @@ q8kv_status q8kv_attn_mass(float *mass, const float *q, const float *lse, const 
     p.errors = dev->errors;
     // Up to 8 warps: the heads in the fewest even passes (a pass holds the query rows of its
     // heads, at most 256 of them, in shared memory), the tokens split over the warps left.
-    p.quads = (p.R + 3) / 4;
-    int most = 256 / (4 * p.quads);
+    p.rows = p.R <= 4 ? 4 : (p.R + 7) & ~7;
+    int most = 256 / p.rows;
     most = most > kMassMaxWarps ? kMassMaxWarps : (most < 1 ? 1 : most);
     const int passes = (n_kv_heads + most - 1) / most;
     p.heads_pass = (n_kv_heads + passes - 1) / passes;
     p.subs = kMassMaxWarps / p.heads_pass;
     const int warps = p.heads_pass * p.subs;
-    // up to 8 query rows per KV head stay in registers; more are read back per tile
-    if (p.quads == 1)
-        return launch_mass<1>(p, dev, warps, stream);
-    if (p.quads == 2)
-        return launch_mass<2>(p, dev, warps, stream);
-    return launch_mass<0>(p, dev, warps, stream);
+    if (p.R <= 4)
+        return launch_mass<kMassQuad>(p, dev, warps, stream);
+    if (p.R <= 8)
+        return launch_mass<kMassOct>(p, dev, warps, stream);
+    return launch_mass<kMassOcts>(p, dev, warps, stream);
 }
 
 } // extern "C"
