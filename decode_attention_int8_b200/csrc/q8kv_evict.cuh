@@ -10,13 +10,15 @@
 //
 // evict_select_kernel finds the set. The threshold (the last mass that stays) comes from
 // a radix selection over the order-preserving 32-bit key of the mass: three histograms (11, 11
-// and 10 bits) instead of a sort; then one pass counts, and one pass writes, the positions above
-// the threshold and the first of those equal to it. A block takes a (sequence, head), or a
-// cluster of up to 8 when there are few of them or their masses do not fit one block's shared
-// memory: the masses are read once, and the blocks' histograms are added up through distributed
-// shared memory. Its time is latency (barriers and dependent steps), so loads go 16 at a time and
-// blocks are as large as they get. Several copies of the histogram per block keep equal digits
-// of neighbouring tokens from serialising on one counter.
+// and 10 bits) instead of a sort; then one pass marks the positions above the threshold and those
+// equal to it (two bits each), and one writes the former and the first of the latter. A block
+// takes a (sequence, head), or a cluster of up to 8 when there are few of them or their keys
+// do not fit one block's shared memory: the masses are read once, counted in the first
+// histogram as they arrive and kept as keys, and the blocks' histograms are added up through
+// distributed shared memory. Its time is issue slots and latency (barriers, dependent steps),
+// so loads go 16 at a time and blocks are as large as they get. The first histogram, which
+// counts every token, has several copies, so that equal digits of neighbouring tokens do not
+// serialise on one counter; the others count the few tokens of one digit.
 //
 // evict_move_kernel copies. A warp takes 32 rows: each lane looks up one row's place (position,
 // two table entries) and moves its scales, then the warp moves the rows, D / 16 lanes of 16 bytes
@@ -52,7 +54,7 @@ struct EvictParams {
     float *ks, *vs;
     int B, Hk, D, bs, mbps, new_mbps, num_blocks, keep, sink, recent;
     int cap, new_cap;       // tokens per row of mass and of new_mass
-    int in_smem;            // a block's masses fit its shared memory
+    int in_smem;            // a block's keys fit its shared memory
     unsigned *errors;
 };
 
@@ -66,7 +68,7 @@ __device__ __forceinline__ uint32_t mass_key(float x)
 }
 
 struct EvictShared {
-    uint32_t copies[kEvictCopies][kEvictBins];
+    uint32_t copies[kEvictCopies][kEvictBins]; // first counts; then the rows' marks
     uint32_t hist[2][kEvictBins]; // this block's counts, read by the cluster
     uint32_t warp_sum[kEvictWarps];
     uint32_t digit, rest;         // chosen digit; tokens still wanted within it
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kEvictThreads)
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) uint8_t esm[];
     EvictShared &sh = *reinterpret_cast<EvictShared *>(esm);
-    float *buf = reinterpret_cast<float *>(esm + sizeof(EvictShared));
+    uint32_t *keys = reinterpret_cast<uint32_t *>(esm + sizeof(EvictShared));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int pair = blockIdx.x / cs;
@@ -197,93 +199,108 @@ __global__ void __launch_bounds__(kEvictThreads)
     const int per = ((L + cs - 1) / cs + 31) & ~31;
     const int lo = rank * per < L ? rank * per : L;
     const int hi = lo + per < L ? lo + per : L;
-    const int mid0 = p.sink, mid1 = L - p.recent;
+    const int n = hi - lo;
+    // [a, z): the block's part of them, counted from lo
+    const int a = min(max(p.sink - lo, 0), n), z = max(min(L - p.recent - lo, n), a);
+    uint32_t wanted = (uint32_t)(p.keep - p.sink - p.recent);
     const float *src = mass + lo; // position lo + i at src[i]
-    if (p.in_smem) {
-        const int n = hi - lo;
+    auto key_at = [&](int i) { return p.in_smem ? keys[i] : mass_key(__ldg(src + i)); };
+
+    // ---- keys, and their first digits
+#pragma unroll
+    for (int i = 0; i < kEvictCopies * kEvictBins / 4 / kEvictThreads; ++i)
+        reinterpret_cast<uint4 *>(&sh.copies[0][0])[i * kEvictThreads + tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    {
         constexpr int kBatch = 16;
+        uint32_t *mine = sh.copies[lane % kEvictCopies];
 #pragma unroll 1
         for (int i0 = tid; i0 < n; i0 += kBatch * kEvictThreads) {
             float v[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (i0 + u * kEvictThreads < n)
-                    v[u] = __ldg(src + i0 + u * kEvictThreads);
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + u * kEvictThreads;
+                v[u] = i < n ? __ldg(src + i) : 0.f;
+            }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (i0 + u * kEvictThreads < n)
-                    buf[i0 + u * kEvictThreads] = v[u];
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + u * kEvictThreads;
+                const uint32_t key = mass_key(v[u]);
+                if (p.in_smem && i < n)
+                    keys[i] = key;
+                if (i >= a && i < z)
+                    atomicAdd(mine + (key >> 21), 1u);
+            }
         }
-        src = buf;
     }
+    __syncthreads();
 
     // ---- threshold key T, and how many tokens equal to it stay
     uint32_t T = 0xffffffffu, ties = 0;
-    uint32_t wanted = (uint32_t)(p.keep - p.sink - p.recent);
     if (wanted > 0) { // (the same for every block)
-        uint32_t prefix = 0;
-#pragma unroll 1
-        for (int round = 0; round < 3; ++round) {
-            const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
-            const int bins = round == 2 ? 1024 : 2048;
-            const int above = shift + (round == 2 ? 10 : 11); // bits decided so far: 32 - above
 #pragma unroll
-            for (int i = 0; i < kEvictCopies * kEvictBins / 4 / kEvictThreads; ++i)
-                reinterpret_cast<uint4 *>(&sh.copies[0][0])[i * kEvictThreads + tid] =
-                    make_uint4(0, 0, 0, 0);
-            __syncthreads(); // (in the first round: the masses are there, too)
-            uint32_t *mine = sh.copies[lane % kEvictCopies];
-            const int a = (mid0 > lo ? mid0 : lo) - lo, z = (mid1 < hi ? mid1 : hi) - lo;
-#pragma unroll 4
-            for (int i = a + tid; i < z; i += kEvictThreads) {
-                const uint32_t key = mass_key(src[i]);
-                if (round == 0 || (key >> above) == prefix)
-                    atomicAdd(mine + ((key >> shift) & (uint32_t)(bins - 1)), 1u);
-            }
-            __syncthreads();
-            // rounds alternate two buffers: a block that counts round r + 1 has passed the
-            // barrier of round r, after which round r - 1's counts are read no more
-            for (int i = tid; i < bins; i += kEvictThreads) {
-                uint32_t s = 0;
+        for (int i = tid; i < kEvictBins; i += kEvictThreads) {
+            uint32_t s = 0;
 #pragma unroll
-                for (int c = 0; c < kEvictCopies; ++c)
-                    s += sh.copies[c][i];
-                sh.hist[round & 1][i] = s;
-            }
-            cluster_barrier(cluster, cs);
-            pick_digit(cluster, sh, round & 1, bins, wanted, tid);
-            prefix = (prefix << (round == 2 ? 10 : 11)) | sh.digit;
-            wanted = sh.rest;
+            for (int c = 0; c < kEvictCopies; ++c)
+                s += sh.copies[c][i];
+            sh.hist[0][i] = s;
+            sh.hist[1][i] = 0; // (for the second digit)
         }
-        T = prefix;
-        ties = wanted;
+        cluster_barrier(cluster, cs);
+        pick_digit(cluster, sh, 0, 2048, wanted, tid);
+        uint32_t prefix = sh.digit;
+        wanted = sh.rest;
+#pragma unroll 4
+        for (int i = a + tid; i < z; i += kEvictThreads) {
+            const uint32_t key = key_at(i);
+            if ((key >> 21) == prefix)
+                atomicAdd(&sh.hist[1][(key >> 10) & 2047u], 1u);
+        }
+        // (every block has passed the barrier below once the third counts begin, so the first
+        // ones, whose place they take, are read no more: cleared after it)
+        cluster_barrier(cluster, cs);
+        pick_digit(cluster, sh, 1, 2048, wanted, tid);
+        prefix = (prefix << 11) | sh.digit;
+        wanted = sh.rest;
+        if (tid < 1024)
+            sh.hist[0][tid] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int i = a + tid; i < z; i += kEvictThreads) {
+            const uint32_t key = key_at(i);
+            if ((key >> 10) == prefix)
+                atomicAdd(&sh.hist[0][key & 1023u], 1u);
+        }
+        cluster_barrier(cluster, cs);
+        pick_digit(cluster, sh, 0, 1024, wanted, tid);
+        T = (prefix << 10) | sh.digit;
+        ties = sh.rest;
     }
 
-    // ---- count, then write: warp w takes a contiguous run of positions
-    if (p.keep == p.sink + p.recent)
-        __syncthreads(); // (no round above has waited for the masses)
-    const int rows = (hi - lo + 31) >> 5;
+    // ---- mark: warp w takes a contiguous run of rows of 32 positions; the marks of a row are two
+    // words in the histogram copies' place (kEvictCopies * kEvictBins / 2 rows at most, else
+    // worked out again)
+    const int rows = (n + 31) >> 5;
+    const bool marked = rows <= kEvictCopies * kEvictBins / 2;
+    uint2 *marks = reinterpret_cast<uint2 *>(&sh.copies[0][0]);
     const int r0 = rows * warp / kEvictWarps, r1 = rows * (warp + 1) / kEvictWarps;
-    auto classify = [&](int i, float &x, bool &gt, bool &eq) {
-        gt = eq = false;
-        x = 0.f;
-        if (i < hi - lo) {
-            const int t = lo + i;
-            x = src[i];
-            const uint32_t key = mass_key(x);
-            const bool held = t < mid0 || t >= mid1;
-            gt = held || (p.keep > p.sink + p.recent && key > T);
-            eq = !held && ties > 0 && key == T;
-        }
+    auto mark = [&](int r) {
+        const int i = r * 32 + lane;
+        const bool in = i < n, held = in && (i < a || i >= z);
+        const uint32_t key = in ? key_at(i) : 0u;
+        const bool gt = held || (in && key > T);
+        const bool eq = in && !held && ties > 0 && key == T;
+        return make_uint2(__ballot_sync(0xffffffffu, gt), __ballot_sync(0xffffffffu, eq));
     };
     uint32_t ngt = 0, neq = 0;
 #pragma unroll 4
     for (int r = r0; r < r1; ++r) {
-        float x;
-        bool gt, eq;
-        classify(r * 32 + lane, x, gt, eq);
-        ngt += __popc(__ballot_sync(0xffffffffu, gt));
-        neq += __popc(__ballot_sync(0xffffffffu, eq));
+        const uint2 m = mark(r);
+        if (marked && lane == 0)
+            marks[r] = m;
+        ngt += __popc(m.x);
+        neq += __popc(m.y);
     }
     if (lane == 0) {
         sh.gt[warp] = ngt;
@@ -295,11 +312,11 @@ __global__ void __launch_bounds__(kEvictThreads)
     const uint32_t og = wg, oe = we;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t a = __shfl_up_sync(0xffffffffu, wg, o);
-        const uint32_t c = __shfl_up_sync(0xffffffffu, we, o);
+        const uint32_t x = __shfl_up_sync(0xffffffffu, wg, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, we, o);
         if (lane >= o) {
-            wg += a;
-            we += c;
+            wg += x;
+            we += y;
         }
     }
     if (tid == 31) {
@@ -326,19 +343,18 @@ __global__ void __launch_bounds__(kEvictThreads)
         }
     }
     const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int r = r0; r < r1; ++r) {
-        float x;
-        bool gt, eq;
-        classify(r * 32 + lane, x, gt, eq);
-        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        const uint32_t e = eq_before + __popc(me & below);
-        const uint32_t pos = gt_before + __popc(mg & below) + (e < ties ? e : ties);
-        if (gt || (eq && e < ties)) {
+        const uint2 m = marked ? marks[r] : mark(r);
+        const uint32_t e = eq_before + __popc(m.y & below);
+        const bool take = (m.x >> lane & 1u) || ((m.y >> lane & 1u) && e < ties);
+        if (take) {
+            const uint32_t pos = gt_before + __popc(m.x & below) + (e < ties ? e : ties);
             kept[pos] = lo + r * 32 + lane;
-            new_mass[pos] = x;
+            new_mass[pos] = __ldg(src + r * 32 + lane);
         }
-        gt_before += __popc(mg);
-        eq_before += __popc(me);
+        gt_before += __popc(m.x);
+        eq_before += __popc(m.y);
     }
     if (cs > 1)
         cluster.sync(); // no block leaves while its counts are read
