@@ -342,25 +342,30 @@ _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # q8kv_dtype
 
 
 def _addr(t, name, dtype, shape, device):
-    """Data pointer of a contiguous tensor of this type and shape on CUDA device `device` (an
-    index). One round of checks per tensor: a small call's time is the host's."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or \
-            not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on "
-                         f"cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    """Data pointer of a contiguous tensor of this type and shape (None: the caller took its
+    sizes from it) on CUDA device `device` (an index). A small call's time is the host's, so the
+    checks are few and the message is made only when one fails."""
+    try:
+        if t.dtype is dtype and (shape is None or t.shape == shape) and \
+                t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor "
+                     f"{tuple(t.shape if shape is None else shape)} on cuda:{device}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
-def _cuda_index(t, name, ndim):
-    """Device index of the tensor that gives a call its sizes."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dim() != ndim:
-        raise ValueError(f"{name}: expected a CUDA tensor with {ndim} dims, got "
-                         f"{tuple(t.shape)} on {t.device}")
-    return t.get_device()
+def _cuda_index(t, name):
+    """Device index of the tensor that says where a call runs."""
+    try:
+        device = t.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if device < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return device
 
 
 def _launch(name, device, stream, *args):
@@ -387,10 +392,8 @@ def q8kv_decode_attn_lse(out, lse, q, k_blocks, v_blocks, kscale, vscale, block_
     every row to lse [B][n_queries][Hq] (-inf for a row that sees no token). ``workspace``: a
     CUDA tensor of q8kv_workspace_bytes(B, n_queries * Hq, Hk, D) bytes, or None for the
     library-managed one."""
-    dev = _cuda_index(q, "q", 4)
-    _cuda_index(k_blocks, "k_blocks", 4)
-    _cuda_index(block_table, "block_table", 2)
-    B, nq, Hq, D = q.shape
+    dev = _cuda_index(q, "q")
+    B, nq, Hq, D = shape = q.shape
     P, bs, Hk, _ = pool = k_blocks.shape
     mbps = block_table.shape[1]
     wptr, nbytes = None, 0
@@ -398,8 +401,8 @@ def q8kv_decode_attn_lse(out, lse, q, k_blocks, v_blocks, kscale, vscale, block_
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
         wptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch("q8kv_decode_attn_lse", dev, stream, _addr(out, "out", _F32, q.shape, dev),
-            _addr(lse, "lse", _F32, (B, nq, Hq), dev), _addr(q, "q", _F32, q.shape, dev),
+    _launch("q8kv_decode_attn_lse", dev, stream, _addr(out, "out", _F32, shape, dev),
+            _addr(lse, "lse", _F32, (B, nq, Hq), dev), _addr(q, "q", _F32, None, dev),
             _addr(k_blocks, "k_blocks", _I8, (P, bs, Hk, D), dev),
             _addr(v_blocks, "v_blocks", _I8, pool, dev),
             _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
@@ -415,14 +418,12 @@ def q8kv_attn_mass(mass, q, lse, k_blocks, kscale, block_table, seq_lens, scale,
     """mass[b][kv][t] = decay * mass[b][kv][t] + sum over the head's query rows of
     exp(score - lse): mass fp32 [B][Hk][max_blocks * block_size], q [B][n_queries][Hq][D], lse
     [B][n_queries][Hq] as q8kv_decode_attn_lse left it."""
-    dev = _cuda_index(q, "q", 4)
-    _cuda_index(k_blocks, "k_blocks", 4)
-    _cuda_index(block_table, "block_table", 2)
+    dev = _cuda_index(q, "q")
     B, nq, Hq, D = q.shape
     P, bs, Hk, _ = k_blocks.shape
     mbps = block_table.shape[1]
     _launch("q8kv_attn_mass", dev, stream, _addr(mass, "mass", _F32, (B, Hk, mbps * bs), dev),
-            _addr(q, "q", _F32, q.shape, dev), _addr(lse, "lse", _F32, (B, nq, Hq), dev),
+            _addr(q, "q", _F32, None, dev), _addr(lse, "lse", _F32, (B, nq, Hq), dev),
             _addr(k_blocks, "k_blocks", _I8, (P, bs, Hk, D), dev),
             _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
             _addr(block_table, "block_table", _I32, (B, mbps), dev),
@@ -437,14 +438,11 @@ def q8kv_evict(k_blocks, v_blocks, kscale, vscale, new_mass, kept, new_lens, mas
     ``recent``, the heaviest others -- and move their rows, in order, to the blocks of
     new_block_table. Writes new_mass fp32 [B][Hk][new_max_blocks * block_size], kept int32
     [B][Hk][keep] (old positions, then -1) and new_lens int32 [B]."""
-    dev = _cuda_index(k_blocks, "k_blocks", 4)
-    _cuda_index(kept, "kept", 3)
-    _cuda_index(block_table, "block_table", 2)
-    _cuda_index(new_block_table, "new_block_table", 2)
+    dev = _cuda_index(k_blocks, "k_blocks")
     P, bs, Hk, D = pool = k_blocks.shape
     B, mbps = block_table.shape
     new_mbps, keep = new_block_table.shape[1], kept.shape[2]
-    _launch("q8kv_evict", dev, stream, _addr(k_blocks, "k_blocks", _I8, pool, dev),
+    _launch("q8kv_evict", dev, stream, _addr(k_blocks, "k_blocks", _I8, None, dev),
             _addr(v_blocks, "v_blocks", _I8, pool, dev),
             _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
             _addr(vscale, "vscale", _F32, (P, bs, Hk), dev),
@@ -452,7 +450,7 @@ def q8kv_evict(k_blocks, v_blocks, kscale, vscale, new_mass, kept, new_lens, mas
             _addr(kept, "kept", _I32, (B, Hk, keep), dev),
             _addr(new_lens, "new_lens", _I32, (B,), dev),
             _addr(mass, "mass", _F32, (B, Hk, mbps * bs), dev),
-            _addr(block_table, "block_table", _I32, (B, mbps), dev),
+            _addr(block_table, "block_table", _I32, None, dev),
             _addr(seq_lens, "seq_lens", _I32, (B,), dev),
             _addr(new_block_table, "new_block_table", _I32, (B, new_mbps), dev), B, Hk, D, bs,
             mbps, new_mbps, P, keep, sink, recent)
@@ -482,13 +480,10 @@ def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_ne
     alike). positions int32 [n_axes][n]; cos_sin fp32 [max_position][rotary_dim], cosines then
     sines; pair_axis: the axis of each of the rotary_dim / 2 pairs (a host sequence or bytes),
     None for one axis; adjacent: pairs (2p, 2p + 1) instead of (p, p + rotary_dim / 2)."""
-    dev = _cuda_index(q_out, "q_out", 3)
-    _cuda_index(k_blocks, "k_blocks", 4)
-    _cuda_index(positions, "positions", 2)
-    _cuda_index(cos_sin, "cos_sin", 2)
+    dev = _cuda_index(q_out, "q_out")
     P, bs, Hk, D = pool = k_blocks.shape
     n, Hq, _ = q_out.shape
-    axes = positions.shape[0]
+    axes, _ = positions.shape
     dtype = q_new.dtype
     code = _DTYPES.get(dtype)
     if code is None:
@@ -505,13 +500,13 @@ def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_ne
         if len(axis) != rot // 2:
             raise ValueError(f"pair_axis needs {rot // 2} entries, got {len(axis)}")
     _launch("q8kv_rope_cache_write", dev, stream, _addr(q_out, "q_out", _F32, (n, Hq, D), dev),
-            _addr(k_blocks, "k_blocks", _I8, pool, dev),
+            _addr(k_blocks, "k_blocks", _I8, None, dev),
             _addr(v_blocks, "v_blocks", _I8, pool, dev),
             _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
             _addr(vscale, "vscale", _F32, (P, bs, Hk), dev), qp, kp, vp,
             _addr(slot_mapping, "slot_mapping", _I64, (n,), dev),
             _addr(positions, "positions", _I32, (axes, n), dev),
-            _addr(cos_sin, "cos_sin", _F32, (max_position, rot), dev), axis, n, axes, Hq, Hk, D,
+            _addr(cos_sin, "cos_sin", _F32, None, dev), axis, n, axes, Hq, Hk, D,
             rot, 1 if adjacent else 0, max_position, code, bs, P, q_stride, kv_stride)
     return q_out
 
@@ -540,7 +535,7 @@ def q8kv_verify_draft(n_accepted, tokens, target_probs, draft_probs, draft_token
     probabilities), draft_tokens int32 [B][n], uniforms fp32 [B][n + 1] (the last one draws),
     n_drafts int32 [B] or None. Writes n_accepted int32 [B] and tokens int32 [B][n + 1]: the
     accepted drafts, the drawn token, then -1."""
-    dev = _cuda_index(target_probs, "target_probs", 3)
+    dev = _cuda_index(target_probs, "target_probs")
     B, n1, vocab = target_probs.shape
     n = n1 - 1
     dtype = target_probs.dtype

@@ -10,15 +10,17 @@
 //
 // evict_select_kernel finds the set. The threshold (the last mass that stays) comes from
 // a radix selection over the order-preserving 32-bit key of the mass: three histograms (11, 11
-// and 10 bits) instead of a sort; then one pass marks the positions above the threshold and those
-// equal to it (two bits each), and one writes the former and the first of the latter. A block
-// takes a (sequence, head), or a cluster of up to 8 when there are few of them or their keys
-// do not fit one block's shared memory: the masses are read once, counted in the first
-// histogram as they arrive and kept as keys, and the blocks' histograms are added up through
-// distributed shared memory. Its time is issue slots and latency (barriers, dependent steps),
-// so loads go 16 at a time and blocks are as large as they get. The first histogram, which
-// counts every token, has several copies, so that equal digits of neighbouring tokens do not
-// serialise on one counter; the others count the few tokens of one digit.
+// and 10 bits) instead of a sort; then one pass counts the positions above the threshold and
+// those equal to it, and one writes the former and the first of the latter. A block takes a
+// (sequence, head), or a cluster of up to 8 when there are few of them or their keys do not
+// fit one block's shared memory: the masses are read once, counted in the first histogram
+// as they arrive and kept as keys, and the blocks' histograms are added up through distributed
+// shared memory. What bounds it is issue slots (a few dozen instructions a position) and, for
+// short sequences, barriers: so a thread takes four neighbouring positions at a time, and counts
+// stay per lane until the end of a pass. The first histogram, which counts every token, has
+// several copies, so that equal digits of neighbouring tokens do not serialise on one counter;
+// the others count the few tokens of one digit. (16 x 8 heads of 16384 positions: 22.3 us with
+// one position per lane, ballots and three passes over copied histograms.)
 //
 // evict_move_kernel copies. A warp takes 32 rows: each lane looks up one row's place (position,
 // two table entries) and moves its scales, then the warp moves the rows, D / 16 lanes of 16 bytes
@@ -37,7 +39,7 @@ namespace q8kv {
 
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
-static_assert(kEvictWarps == 32, "one lane per warp in the block-wide scans");
+static_assert(kEvictWarps <= 32 && kEvictThreads >= 256, "one lane per warp in the block-wide sums");
 constexpr int kEvictCluster = 8;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictCopies = 4; // histogram copies per block
@@ -54,7 +56,6 @@ struct EvictParams {
     float *ks, *vs;
     int B, Hk, D, bs, mbps, new_mbps, num_blocks, keep, sink, recent;
     int cap, new_cap;       // tokens per row of mass and of new_mass
-    int in_smem;            // a block's keys fit its shared memory
     unsigned *errors;
 };
 
@@ -68,9 +69,9 @@ __device__ __forceinline__ uint32_t mass_key(float x)
 }
 
 struct EvictShared {
-    uint32_t copies[kEvictCopies][kEvictBins]; // first counts; then the rows' marks
+    uint32_t copies[kEvictCopies][kEvictBins];
     uint32_t hist[2][kEvictBins]; // this block's counts, read by the cluster
-    uint32_t warp_sum[kEvictWarps];
+    uint32_t warp_sum[8];
     uint32_t digit, rest;         // chosen digit; tokens still wanted within it
     uint32_t gt[kEvictWarps], eq[kEvictWarps];
     uint32_t total_gt, total_eq;  // this block's counts, read by the cluster
@@ -85,76 +86,67 @@ __device__ __forceinline__ void cluster_barrier(cooperative_groups::cluster_grou
 }
 
 // Digit of the wanted-th largest key among the counted ones: the bin where the running count
-// from the top reaches `wanted`. Every block of the cluster computes it from all histograms.
+// from the top reaches `wanted`. Every block of the cluster computes it from all histograms:
+// 256 threads, 8 bins each, the highest bins first.
 __device__ __forceinline__ void pick_digit(cooperative_groups::cluster_group &cluster,
                                            EvictShared &sh, int buf, int bins, uint32_t wanted,
-                                           int tid)
+                                           int tid, int cs)
 {
+    constexpr int kPer = 8, kThreads = kEvictBins / kPer, kWarps = kThreads / 32;
     const int lane = tid & 31, warp = tid >> 5;
-    const int cs = (int)cluster.num_blocks();
-    constexpr int kPer = kEvictBins / kEvictThreads;
-    uint32_t n[kPer];
-    uint32_t sum = 0;
-    // thread t: bins bins - 1 - kPer t - i, i = 0 .. kPer - 1
+    uint32_t n[kPer]; // n[i]: bin low + i
+    uint32_t sum = 0, incl = 0;
+    const int low = bins - kPer * (tid + 1);
+    if (tid < kThreads) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        n[i] = 0;
-    const int top = bins - 1 - kPer * tid;
-    if (top >= 0) {
-        if (cs == 1) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                n[i] = sh.hist[buf][top - i];
-        } else {
-            uint32_t v[kEvictCluster][kPer]; // all blocks' counts in flight at once
-#pragma unroll
-            for (int r = 0; r < kEvictCluster; ++r) {
-                const uint32_t *h = cluster.map_shared_rank(&sh.hist[buf][0], r < cs ? r : 0);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    v[r][i] = r < cs ? h[top - i] : 0;
+        for (int i = 0; i < kPer; ++i)
+            n[i] = 0;
+        if (low >= 0) {
+#pragma unroll 2
+            for (int r = 0; r < cs; ++r) {
+                const uint32_t *h = cs == 1 ? sh.hist[buf]
+                                            : cluster.map_shared_rank(&sh.hist[buf][0], r);
+                const uint4 x = *reinterpret_cast<const uint4 *>(h + low);
+                const uint4 y = *reinterpret_cast<const uint4 *>(h + low + 4);
+                n[0] += x.x, n[1] += x.y, n[2] += x.z, n[3] += x.w;
+                n[4] += y.x, n[5] += y.y, n[6] += y.z, n[7] += y.w;
             }
-#pragma unroll
-            for (int r = 0; r < kEvictCluster; ++r)
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    n[i] += v[r][i];
         }
-    }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        sum += n[i];
-    uint32_t incl = sum;
+        for (int i = 0; i < kPer; ++i)
+            sum += n[i];
+        incl = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += t;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += t;
+        }
+        if (lane == 31)
+            sh.warp_sum[warp] = incl;
     }
-    if (lane == 31)
-        sh.warp_sum[warp] = incl;
     __syncthreads();
-    // (one value per warp and lane: the warps' sums are added by one more warp scan)
-    uint32_t ws = sh.warp_sum[lane];
-    const uint32_t own = ws;
+    if (tid < kThreads) {
+        uint32_t run = incl - sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, ws, o);
-        if (lane >= o)
-            ws += t;
-    }
-    uint32_t run = incl - sum + __shfl_sync(0xffffffffu, ws - own, warp);
+        for (int w = 0; w < kWarps; ++w)
+            run += w < warp ? sh.warp_sum[w] : 0;
+        if (run < wanted && wanted <= run + sum) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (run < wanted && wanted <= run + n[i]) {
-            sh.digit = (uint32_t)(top - i);
-            sh.rest = wanted - run;
+            for (int i = kPer - 1; i >= 0; --i) {
+                if (run < wanted && wanted <= run + n[i]) {
+                    sh.digit = (uint32_t)(low + i);
+                    sh.rest = wanted - run;
+                }
+                run += n[i];
+            }
         }
-        run += n[i];
     }
     __syncthreads();
 }
 
+// SMEM: the block's keys stay in shared memory; otherwise they are made again from the masses.
+template <bool SMEM>
 __global__ void __launch_bounds__(kEvictThreads)
     evict_select_kernel(const __grid_constant__ EvictParams p)
 {
@@ -195,16 +187,27 @@ __global__ void __launch_bounds__(kEvictThreads)
         return;
     }
 
-    // this block's positions [lo, hi); the chosen ones come from [mid0, mid1)
+    // this block's positions [lo, lo + n); the chosen ones are among [a, z), counted from lo
     const int per = ((L + cs - 1) / cs + 31) & ~31;
     const int lo = rank * per < L ? rank * per : L;
-    const int hi = lo + per < L ? lo + per : L;
-    const int n = hi - lo;
-    // [a, z): the block's part of them, counted from lo
+    const int n = (lo + per < L ? lo + per : L) - lo;
     const int a = min(max(p.sink - lo, 0), n), z = max(min(L - p.recent - lo, n), a);
     uint32_t wanted = (uint32_t)(p.keep - p.sink - p.recent);
     const float *src = mass + lo; // position lo + i at src[i]
-    auto key_at = [&](int i) { return p.in_smem ? keys[i] : mass_key(__ldg(src + i)); };
+    // keys of positions i .. i + 3 (i a multiple of 4); past the last one: 0, below every key
+    auto load4 = [&](int i) {
+        uint32_t k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            k[u] = i + u < n ? mass_key(__ldg(src + i + u)) : 0u;
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    };
+    auto keys4 = [&](int i) {
+        if constexpr (SMEM)
+            return *reinterpret_cast<const uint4 *>(keys + i);
+        else
+            return load4(i);
+    };
 
     // ---- keys, and their first digits
 #pragma unroll
@@ -212,24 +215,33 @@ __global__ void __launch_bounds__(kEvictThreads)
         reinterpret_cast<uint4 *>(&sh.copies[0][0])[i * kEvictThreads + tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     {
-        constexpr int kBatch = 16;
         uint32_t *mine = sh.copies[lane % kEvictCopies];
+        constexpr int kBatch = 4; // 16 loads in flight
 #pragma unroll 1
-        for (int i0 = tid; i0 < n; i0 += kBatch * kEvictThreads) {
-            float v[kBatch];
+        for (int i0 = 4 * tid; i0 < n; i0 += 4 * kBatch * kEvictThreads) {
+            uint4 k[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                k[u] = load4(i0 + 4 * u * kEvictThreads);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                const int i = i0 + u * kEvictThreads;
-                v[u] = i < n ? __ldg(src + i) : 0.f;
-            }
+                const int i = i0 + 4 * u * kEvictThreads;
+                if (i >= n)
+                    break;
+                if constexpr (SMEM)
+                    *reinterpret_cast<uint4 *>(keys + i) = k[u];
+                if (i >= a && i + 4 <= z) {
+                    atomicAdd(mine + (k[u].x >> 21), 1u);
+                    atomicAdd(mine + (k[u].y >> 21), 1u);
+                    atomicAdd(mine + (k[u].z >> 21), 1u);
+                    atomicAdd(mine + (k[u].w >> 21), 1u);
+                } else {
+                    const uint32_t x[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int i = i0 + u * kEvictThreads;
-                const uint32_t key = mass_key(v[u]);
-                if (p.in_smem && i < n)
-                    keys[i] = key;
-                if (i >= a && i < z)
-                    atomicAdd(mine + (key >> 21), 1u);
+                    for (int e = 0; e < 4; ++e)
+                        if (i + e >= a && i + e < z)
+                            atomicAdd(mine + (x[e] >> 21), 1u);
+                }
             }
         }
     }
@@ -247,85 +259,90 @@ __global__ void __launch_bounds__(kEvictThreads)
             sh.hist[0][i] = s;
             sh.hist[1][i] = 0; // (for the second digit)
         }
+        // counts of the keys whose bits from `above` up are `prefix`, by their bits from `shift`
+        auto count = [&](uint32_t *hist, uint32_t prefix, int above, int shift, uint32_t mask) {
+#pragma unroll 2
+            for (int i = 4 * tid; i < z; i += 4 * kEvictThreads) {
+                const uint4 k = keys4(i);
+                const uint32_t x[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((x[e] >> above) == prefix && i + e >= a && i + e < z)
+                        atomicAdd(hist + ((x[e] >> shift) & mask), 1u);
+            }
+        };
         cluster_barrier(cluster, cs);
-        pick_digit(cluster, sh, 0, 2048, wanted, tid);
+        pick_digit(cluster, sh, 0, 2048, wanted, tid, cs);
         uint32_t prefix = sh.digit;
         wanted = sh.rest;
-#pragma unroll 4
-        for (int i = a + tid; i < z; i += kEvictThreads) {
-            const uint32_t key = key_at(i);
-            if ((key >> 21) == prefix)
-                atomicAdd(&sh.hist[1][(key >> 10) & 2047u], 1u);
-        }
-        // (every block has passed the barrier below once the third counts begin, so the first
-        // ones, whose place they take, are read no more: cleared after it)
+        count(sh.hist[1], prefix, 21, 10, 2047u);
+        // (every block is past its reads of the first counts, whose place the third ones take,
+        // once it has come to this barrier: they are cleared after it)
         cluster_barrier(cluster, cs);
-        pick_digit(cluster, sh, 1, 2048, wanted, tid);
+        pick_digit(cluster, sh, 1, 2048, wanted, tid, cs);
         prefix = (prefix << 11) | sh.digit;
         wanted = sh.rest;
-        if (tid < 1024)
-            sh.hist[0][tid] = 0;
+        for (int i = tid; i < 1024; i += kEvictThreads)
+            sh.hist[0][i] = 0;
         __syncthreads();
-#pragma unroll 4
-        for (int i = a + tid; i < z; i += kEvictThreads) {
-            const uint32_t key = key_at(i);
-            if ((key >> 10) == prefix)
-                atomicAdd(&sh.hist[0][key & 1023u], 1u);
-        }
+        count(sh.hist[0], prefix, 10, 0, 1023u);
         cluster_barrier(cluster, cs);
-        pick_digit(cluster, sh, 0, 1024, wanted, tid);
+        pick_digit(cluster, sh, 0, 1024, wanted, tid, cs);
         T = (prefix << 10) | sh.digit;
         ties = sh.rest;
     }
 
-    // ---- mark: warp w takes a contiguous run of rows of 32 positions; the marks of a row are two
-    // words in the histogram copies' place (kEvictCopies * kEvictBins / 2 rows at most, else
-    // worked out again)
-    const int rows = (n + 31) >> 5;
-    const bool marked = rows <= kEvictCopies * kEvictBins / 2;
-    uint2 *marks = reinterpret_cast<uint2 *>(&sh.copies[0][0]);
-    const int r0 = rows * warp / kEvictWarps, r1 = rows * (warp + 1) / kEvictWarps;
-    auto mark = [&](int r) {
-        const int i = r * 32 + lane;
-        const bool in = i < n, held = in && (i < a || i >= z);
-        const uint32_t key = in ? key_at(i) : 0u;
-        const bool gt = held || (in && key > T);
-        const bool eq = in && !held && ties > 0 && key == T;
-        return make_uint2(__ballot_sync(0xffffffffu, gt), __ballot_sync(0xffffffffu, eq));
+    // ---- count, then write: warp w takes a contiguous run of chunks of 128 positions, a lane
+    // four neighbours of each. Bits 0-3 of a mark: above the threshold (or held); bits 4-7:
+    // equal to it.
+    auto mark = [&](int i) {
+        uint32_t m = 0;
+        if (i < n) {
+            const uint4 k = keys4(i);
+            const uint32_t x[4] = {k.x, k.y, k.z, k.w};
+            if (i >= a && i + 4 <= z) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    m |= (x[e] > T ? 1u << e : 0u) | (x[e] == T ? 16u << e : 0u);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i + e < n) {
+                        if (i + e < a || i + e >= z)
+                            m |= 1u << e;
+                        else
+                            m |= (x[e] > T ? 1u << e : 0u) | (x[e] == T ? 16u << e : 0u);
+                    }
+            }
+        }
+        return m;
     };
+    const int chunks = (n + 127) >> 7;
+    const int c0 = chunks * warp / kEvictWarps, c1 = chunks * (warp + 1) / kEvictWarps;
     uint32_t ngt = 0, neq = 0;
-#pragma unroll 4
-    for (int r = r0; r < r1; ++r) {
-        const uint2 m = mark(r);
-        if (marked && lane == 0)
-            marks[r] = m;
-        ngt += __popc(m.x);
-        neq += __popc(m.y);
+#pragma unroll 2
+    for (int c = c0; c < c1; ++c) {
+        const uint32_t m = mark(c * 128 + 4 * lane);
+        ngt += __popc(m & 15u);
+        neq += __popc(m >> 4);
     }
+    ngt = __reduce_add_sync(0xffffffffu, ngt);
+    neq = __reduce_add_sync(0xffffffffu, neq);
     if (lane == 0) {
         sh.gt[warp] = ngt;
         sh.eq[warp] = neq;
     }
     __syncthreads();
     // counts of the warps before this one, and of the block
-    uint32_t wg = sh.gt[lane], we = sh.eq[lane];
-    const uint32_t og = wg, oe = we;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, wg, o);
-        const uint32_t y = __shfl_up_sync(0xffffffffu, we, o);
-        if (lane >= o) {
-            wg += x;
-            we += y;
-        }
-    }
-    if (tid == 31) {
-        sh.total_gt = wg;
-        sh.total_eq = we;
-    }
-    uint32_t gt_before = __shfl_sync(0xffffffffu, wg - og, warp);
-    uint32_t eq_before = __shfl_sync(0xffffffffu, we - oe, warp);
+    const uint32_t wg = lane < kEvictWarps ? sh.gt[lane] : 0u;
+    const uint32_t we = lane < kEvictWarps ? sh.eq[lane] : 0u;
+    uint32_t gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
+    uint32_t eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
     if (cs > 1) {
+        if (warp == kEvictWarps - 1 && lane == 0) {
+            sh.total_gt = gt_before + ngt;
+            sh.total_eq = eq_before + neq;
+        }
         cluster.sync();
         uint32_t tg[kEvictCluster], te[kEvictCluster];
 #pragma unroll
@@ -342,19 +359,36 @@ __global__ void __launch_bounds__(kEvictThreads)
             eq_before += te[r];
         }
     }
-    const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int r = r0; r < r1; ++r) {
-        const uint2 m = marked ? marks[r] : mark(r);
-        const uint32_t e = eq_before + __popc(m.y & below);
-        const bool take = (m.x >> lane & 1u) || ((m.y >> lane & 1u) && e < ties);
-        if (take) {
-            const uint32_t pos = gt_before + __popc(m.x & below) + (e < ties ? e : ties);
-            kept[pos] = lo + r * 32 + lane;
-            new_mass[pos] = __ldg(src + r * 32 + lane);
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+        const int i = c * 128 + 4 * lane;
+        const uint32_t m = mark(i);
+        // counts of the lanes before this one: above in the low half, equal in the high one
+        const uint32_t own = __popc(m & 15u) | (__popc(m >> 4) << 16);
+        uint32_t incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += t;
         }
-        gt_before += __popc(m.x);
-        eq_before += __popc(m.y);
+        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+        uint32_t g = gt_before + ((incl - own) & 0xffffu), e = eq_before + ((incl - own) >> 16);
+        if (m) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool gt = (m >> u) & 1u, eq = (m >> (4 + u)) & 1u;
+                if (gt || (eq && e < ties)) {
+                    const uint32_t pos = g + (e < ties ? e : ties);
+                    kept[pos] = lo + i + u;
+                    new_mass[pos] = __ldg(src + i + u);
+                }
+                g += gt ? 1u : 0u;
+                e += eq ? 1u : 0u;
+            }
+        }
+        gt_before += all & 0xffffu;
+        eq_before += all >> 16;
     }
     if (cs > 1)
         cluster.sync(); // no block leaves while its counts are read

@@ -74,7 +74,10 @@ q8kv_status q8kv_evict(int8_t *k_blocks, int8_t *v_blocks, float *kscale, float 
             return st;
         const int d = (int)(dev - g_dev);
         if (!g_evict_attr[d]) {
-            Q8KV_CUDA(cudaFuncSetAttribute(evict_select_kernel,
+            Q8KV_CUDA(cudaFuncSetAttribute(evict_select_kernel<true>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           dev->smem_optin));
+            Q8KV_CUDA(cudaFuncSetAttribute(evict_select_kernel<false>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            dev->smem_optin));
             g_evict_attr[d] = true;
@@ -115,9 +118,10 @@ q8kv_status q8kv_evict(int8_t *k_blocks, int8_t *v_blocks, float *kscale, float 
     const size_t room = (size_t)dev->smem_optin - sizeof(EvictShared);
     while (cs < kEvictCluster && part(cs) > room)
         cs *= 2;
-    p.in_smem = part(cs) <= room ? 1 : 0;
-    const size_t smem = sizeof(EvictShared) + (p.in_smem ? part(cs) : 0);
-    st = launch_cluster(evict_select_kernel, p, (unsigned)pairs, cs, kEvictThreads, smem, stream);
+    const bool in_smem = part(cs) <= room;
+    const size_t smem = sizeof(EvictShared) + (in_smem ? part(cs) : 0);
+    st = launch_cluster(in_smem ? evict_select_kernel<true> : evict_select_kernel<false>, p,
+                        (unsigned)pairs, cs, kEvictThreads, smem, stream);
     if (st != Q8KV_OK)
         return st;
     if (head_dim == 64)
