@@ -16,25 +16,27 @@ from ._lib import (  # noqa: F401
     Q8KVError,
     lib,
     lib_path,
-    q8kv_attn_mass,
     q8kv_cache_write,
     q8kv_cache_write_q4,
     q8kv_debug_block_dots,
     q8kv_debug_quantize_q,
     q8kv_debug_stall_pipeline,
     q8kv_decode_attn,
-    q8kv_decode_attn_lse,
     q8kv_decode_attn_multi,
     q8kv_decode_attn_q4,
     q8kv_decode_attn_static,
     q8kv_decode_attn_ws,
-    q8kv_evict,
     q8kv_quest_metadata,
-    q8kv_rope_cache_write,
-    q8kv_verify_draft,
     q8kv_device_errors,
     q8kv_version,
     q8kv_workspace_bytes,
     q8kv_workspace_init,
+)
+from ._serving import (  # noqa: F401
+    q8kv_attn_mass,
+    q8kv_decode_attn_lse,
+    q8kv_evict,
+    q8kv_rope_cache_write,
+    q8kv_verify_draft,
 )
 from . import inputs  # noqa: F401

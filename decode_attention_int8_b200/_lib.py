@@ -338,223 +338,6 @@ def q8kv_quest_metadata(maxblocks, minblocks, k_blocks, kscale, block_table, seq
                                      P, nm, _stream(stream)), "q8kv_quest_metadata")
 
 
-_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # q8kv_dtype
-
-
-def _addr(t, name, dtype, shape, device):
-    """Data pointer of a contiguous tensor of this type and shape (None: the caller took its
-    sizes from it) on CUDA device `device` (an index). A small call's time is the host's, so the
-    checks are few and the message is made only when one fails."""
-    try:
-        if t.dtype is dtype and (shape is None or t.shape == shape) and \
-                t.get_device() == device and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
-    raise ValueError(f"{name}: expected a contiguous {dtype} tensor "
-                     f"{tuple(t.shape if shape is None else shape)} on cuda:{device}, got "
-                     f"{t.dtype} {tuple(t.shape)} on {t.device}"
-                     f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-
-
-def _cuda_index(t, name):
-    """Device index of the tensor that says where a call runs."""
-    try:
-        device = t.get_device()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
-    if device < 0:
-        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
-    return device
-
-
-def _launch(name, device, stream, *args):
-    """Call the entry point `name` on CUDA device `device`, whichever is current: `args`, then
-    the stream (the device's current one by default)."""
-    fn = getattr(_lib or lib(), name)
-    if device != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            status = fn(*args, _stream(stream))
-    elif stream is None:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
-    else:
-        status = fn(*args, _stream(stream))
-    if status:
-        raise Q8KVError(status, name)
-
-
-_F32, _I32, _I64, _I8 = torch.float32, torch.int32, torch.int64, torch.int8
-
-
-def q8kv_decode_attn_lse(out, lse, q, k_blocks, v_blocks, kscale, vscale, block_table, seq_lens,
-                         scale, workspace=None, stream=None):
-    """q8kv_decode_attn_multi (q, out [B][n_queries][Hq][D]) that also writes the log-sum-exp of
-    every row to lse [B][n_queries][Hq] (-inf for a row that sees no token). ``workspace``: a
-    CUDA tensor of q8kv_workspace_bytes(B, n_queries * Hq, Hk, D) bytes, or None for the
-    library-managed one."""
-    dev = _cuda_index(q, "q")
-    B, nq, Hq, D = shape = q.shape
-    P, bs, Hk, _ = pool = k_blocks.shape
-    mbps = block_table.shape[1]
-    wptr, nbytes = None, 0
-    if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-        wptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch("q8kv_decode_attn_lse", dev, stream, _addr(out, "out", _F32, shape, dev),
-            _addr(lse, "lse", _F32, (B, nq, Hq), dev), _addr(q, "q", _F32, None, dev),
-            _addr(k_blocks, "k_blocks", _I8, (P, bs, Hk, D), dev),
-            _addr(v_blocks, "v_blocks", _I8, pool, dev),
-            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
-            _addr(vscale, "vscale", _F32, (P, bs, Hk), dev),
-            _addr(block_table, "block_table", _I32, (B, mbps), dev),
-            _addr(seq_lens, "seq_lens", _I32, (B,), dev), B, nq, Hq, Hk, D, bs, mbps, P, scale,
-            wptr, nbytes)
-    return out
-
-
-def q8kv_attn_mass(mass, q, lse, k_blocks, kscale, block_table, seq_lens, scale, decay=1.0,
-                   stream=None):
-    """mass[b][kv][t] = decay * mass[b][kv][t] + sum over the head's query rows of
-    exp(score - lse): mass fp32 [B][Hk][max_blocks * block_size], q [B][n_queries][Hq][D], lse
-    [B][n_queries][Hq] as q8kv_decode_attn_lse left it."""
-    dev = _cuda_index(q, "q")
-    B, nq, Hq, D = q.shape
-    P, bs, Hk, _ = k_blocks.shape
-    mbps = block_table.shape[1]
-    _launch("q8kv_attn_mass", dev, stream, _addr(mass, "mass", _F32, (B, Hk, mbps * bs), dev),
-            _addr(q, "q", _F32, None, dev), _addr(lse, "lse", _F32, (B, nq, Hq), dev),
-            _addr(k_blocks, "k_blocks", _I8, (P, bs, Hk, D), dev),
-            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
-            _addr(block_table, "block_table", _I32, (B, mbps), dev),
-            _addr(seq_lens, "seq_lens", _I32, (B,), dev), B, nq, Hq, Hk, D, bs, mbps, P, scale,
-            decay)
-    return mass
-
-
-def q8kv_evict(k_blocks, v_blocks, kscale, vscale, new_mass, kept, new_lens, mass, block_table,
-               seq_lens, new_block_table, sink=0, recent=0, stream=None):
-    """Keep kept.shape[2] tokens per (sequence, KV head) -- the first ``sink``, the last
-    ``recent``, the heaviest others -- and move their rows, in order, to the blocks of
-    new_block_table. Writes new_mass fp32 [B][Hk][new_max_blocks * block_size], kept int32
-    [B][Hk][keep] (old positions, then -1) and new_lens int32 [B]."""
-    dev = _cuda_index(k_blocks, "k_blocks")
-    P, bs, Hk, D = pool = k_blocks.shape
-    B, mbps = block_table.shape
-    new_mbps, keep = new_block_table.shape[1], kept.shape[2]
-    _launch("q8kv_evict", dev, stream, _addr(k_blocks, "k_blocks", _I8, None, dev),
-            _addr(v_blocks, "v_blocks", _I8, pool, dev),
-            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
-            _addr(vscale, "vscale", _F32, (P, bs, Hk), dev),
-            _addr(new_mass, "new_mass", _F32, (B, Hk, new_mbps * bs), dev),
-            _addr(kept, "kept", _I32, (B, Hk, keep), dev),
-            _addr(new_lens, "new_lens", _I32, (B,), dev),
-            _addr(mass, "mass", _F32, (B, Hk, mbps * bs), dev),
-            _addr(block_table, "block_table", _I32, None, dev),
-            _addr(seq_lens, "seq_lens", _I32, (B,), dev),
-            _addr(new_block_table, "new_block_table", _I32, (B, new_mbps), dev), B, Hk, D, bs,
-            mbps, new_mbps, P, keep, sink, recent)
-
-
-def _token_rows(t, name, dtype, shape, device):
-    """(data pointer, token stride) of rows [n][heads][D] whose last two dimensions have no
-    gaps."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    n, heads, D = shape
-    strides = t.stride()
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or strides[2] != 1 or \
-            (heads > 1 and strides[1] != D):
-        raise ValueError(f"{name}: expected a {dtype} tensor {tuple(shape)} on cuda:{device} "
-                         f"with contiguous rows, got {t.dtype} {tuple(t.shape)} on {t.device} "
-                         f"with strides {strides}")
-    return t.data_ptr(), strides[0] if n > 1 else heads * D
-
-
-def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_new, v_new,
-                          slot_mapping, positions, cos_sin, pair_axis=None, adjacent=False,
-                          stream=None):
-    """Rotate q_new [n][Hq][D] into q_out (fp32) and k_new [n][Hk][D], and write the rotated keys
-    and v_new to the q8 cache at slot_mapping (int64 [n], negative = padding). q_new, k_new
-    and v_new: one of float32, float16, bfloat16, token dimension strided (k_new and v_new
-    alike). positions int32 [n_axes][n]; cos_sin fp32 [max_position][rotary_dim], cosines then
-    sines; pair_axis: the axis of each of the rotary_dim / 2 pairs (a host sequence or bytes),
-    None for one axis; adjacent: pairs (2p, 2p + 1) instead of (p, p + rotary_dim / 2)."""
-    dev = _cuda_index(q_out, "q_out")
-    P, bs, Hk, D = pool = k_blocks.shape
-    n, Hq, _ = q_out.shape
-    axes, _ = positions.shape
-    dtype = q_new.dtype
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise ValueError(f"q_new: expected float32, float16 or bfloat16, got {dtype}")
-    qp, q_stride = _token_rows(q_new, "q_new", dtype, (n, Hq, D), dev)
-    kp, kv_stride = _token_rows(k_new, "k_new", dtype, (n, Hk, D), dev)
-    vp, v_stride = _token_rows(v_new, "v_new", dtype, (n, Hk, D), dev)
-    if v_stride != kv_stride:
-        raise ValueError("k_new and v_new must have the same token stride")
-    max_position, rot = cos_sin.shape
-    axis = None
-    if pair_axis is not None:
-        axis = bytes(pair_axis)
-        if len(axis) != rot // 2:
-            raise ValueError(f"pair_axis needs {rot // 2} entries, got {len(axis)}")
-    _launch("q8kv_rope_cache_write", dev, stream, _addr(q_out, "q_out", _F32, (n, Hq, D), dev),
-            _addr(k_blocks, "k_blocks", _I8, None, dev),
-            _addr(v_blocks, "v_blocks", _I8, pool, dev),
-            _addr(kscale, "kscale", _F32, (P, bs, Hk), dev),
-            _addr(vscale, "vscale", _F32, (P, bs, Hk), dev), qp, kp, vp,
-            _addr(slot_mapping, "slot_mapping", _I64, (n,), dev),
-            _addr(positions, "positions", _I32, (axes, n), dev),
-            _addr(cos_sin, "cos_sin", _F32, None, dev), axis, n, axes, Hq, Hk, D,
-            rot, 1 if adjacent else 0, max_position, code, bs, P, q_stride, kv_stride)
-    return q_out
-
-
-def _prob_rows(t, name, dtype, shape, device):
-    """(data pointer, elements between rows) of probabilities [B][rows][vocab]."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    B, rows, vocab = shape
-    strides = t.stride()
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or \
-            (vocab > 1 and strides[2] != 1):
-        raise ValueError(f"{name}: expected a {dtype} tensor {tuple(shape)} on cuda:{device} "
-                         f"with contiguous rows, got {t.dtype} {tuple(t.shape)} on {t.device} "
-                         f"with strides {strides}")
-    stride = strides[1] if rows > 1 else (strides[0] if B > 1 else vocab)
-    if rows > 1 and B > 1 and strides[0] != rows * stride:
-        raise ValueError(f"{name}: the rows of consecutive sequences must be evenly spaced")
-    return t.data_ptr(), stride
-
-
-def q8kv_verify_draft(n_accepted, tokens, target_probs, draft_probs, draft_tokens, uniforms,
-                      n_drafts=None, stream=None):
-    """Speculative sampling's accept test and draw: target_probs [B][n + 1][vocab], draft_probs
-    [B][n][vocab] of the same type (float32, float16, bfloat16; None for drafts without
-    probabilities), draft_tokens int32 [B][n], uniforms fp32 [B][n + 1] (the last one draws),
-    n_drafts int32 [B] or None. Writes n_accepted int32 [B] and tokens int32 [B][n + 1]: the
-    accepted drafts, the drawn token, then -1."""
-    dev = _cuda_index(target_probs, "target_probs")
-    B, n1, vocab = target_probs.shape
-    n = n1 - 1
-    dtype = target_probs.dtype
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise ValueError(f"target_probs: expected float32, float16 or bfloat16, got {dtype}")
-    tp, ts = _prob_rows(target_probs, "target_probs", dtype, (B, n1, vocab), dev)
-    dp, ds = None, 0
-    if draft_probs is not None and n:
-        dp, ds = _prob_rows(draft_probs, "draft_probs", dtype, (B, n, vocab), dev)
-    _launch("q8kv_verify_draft", dev, stream,
-            _addr(n_accepted, "n_accepted", _I32, (B,), dev),
-            _addr(tokens, "tokens", _I32, (B, n1), dev), tp, dp,
-            _addr(draft_tokens, "draft_tokens", _I32, (B, n), dev),
-            None if n_drafts is None else _addr(n_drafts, "n_drafts", _I32, (B,), dev),
-            _addr(uniforms, "uniforms", _F32, (B, n1), dev), B, n, vocab, ts, ds, code)
-    return tokens
-
-
 def q8kv_debug_quantize_q(qi, qsc, q, stream=None):
     """int8 codes qi [..., D] and block scales qsc [..., D/32] of the fp32 rows of q [..., D]."""
     D = q.shape[-1]

@@ -1,4 +1,5 @@
-"""Build libq8kv.so (the CUDA library behind include/q8kv.h) in-tree for sm_100a."""
+"""Build libq8kv.so (the CUDA library behind include/q8kv.h) in-tree for sm_100a, and the compiled
+half of its torch binding."""
 from __future__ import annotations
 
 import glob
@@ -6,6 +7,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libq8kv.so")
 MAIN_SRC = os.path.join(CSRC, "q8kv_api.cu")
+BINDING = os.path.join(PKG, "_q8kv_torch.so")
+BINDING_SRC = os.path.join(PKG, "binding", "q8kv_torch.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -54,5 +58,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile binding/q8kv_torch.cpp against the running torch if it is stale."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "q8kv.h")]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(BINDING) >= os.path.getmtime(d) for d in deps):
+        return BINDING
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    lib = os.path.join(torch_dir, "lib")
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    subprocess.check_call([
+        "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
+        "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+        "-isystem", os.path.join(cuda, "include"),
+        "-isystem", sysconfig.get_paths()["include"],
+        BINDING_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_binding(force="--force" in sys.argv))
