@@ -102,14 +102,18 @@ __device__ __forceinline__ void pick_digit(cooperative_groups::cluster_group &cl
         for (int i = 0; i < kPer; ++i)
             n[i] = 0;
         if (low >= 0) {
-#pragma unroll 2
-            for (int r = 0; r < cs; ++r) {
-                const uint32_t *h = cs == 1 ? sh.hist[buf]
-                                            : cluster.map_shared_rank(&sh.hist[buf][0], r);
+            auto add = [&](const uint32_t *h) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(h + low);
                 const uint4 y = *reinterpret_cast<const uint4 *>(h + low + 4);
                 n[0] += x.x, n[1] += x.y, n[2] += x.z, n[3] += x.w;
                 n[4] += y.x, n[5] += y.y, n[6] += y.z, n[7] += y.w;
+            };
+            if (cs == 1) {
+                add(sh.hist[buf]);
+            } else {
+#pragma unroll 2
+                for (int r = 0; r < cs; ++r)
+                    add(cluster.map_shared_rank(&sh.hist[buf][0], r));
             }
         }
 #pragma unroll
@@ -194,13 +198,20 @@ __global__ void __launch_bounds__(kEvictThreads)
     const int a = min(max(p.sink - lo, 0), n), z = max(min(L - p.recent - lo, n), a);
     uint32_t wanted = (uint32_t)(p.keep - p.sink - p.recent);
     const float *src = mass + lo; // position lo + i at src[i]
-    // keys of positions i .. i + 3 (i a multiple of 4); past the last one: 0, below every key
-    auto load4 = [&](int i) {
-        uint32_t k[4];
+    const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0; // 16-byte loads
+    // masses of positions i .. i + 3 (i a multiple of 4); past the last one: NaN
+    auto mass4 = [&](int i) {
+        if (vec && i + 4 <= n)
+            return __ldg(reinterpret_cast<const float4 *>(src + i));
+        float x[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            k[u] = i + u < n ? mass_key(__ldg(src + i + u)) : 0u;
-        return make_uint4(k[0], k[1], k[2], k[3]);
+            x[u] = i + u < n ? __ldg(src + i + u) : __int_as_float(0x7fc00000);
+        return make_float4(x[0], x[1], x[2], x[3]);
+    };
+    auto load4 = [&](int i) {
+        const float4 x = mass4(i);
+        return make_uint4(mass_key(x.x), mass_key(x.y), mass_key(x.z), mass_key(x.w));
     };
     auto keys4 = [&](int i) {
         if constexpr (SMEM)
@@ -219,24 +230,24 @@ __global__ void __launch_bounds__(kEvictThreads)
         constexpr int kBatch = 4; // 16 loads in flight
 #pragma unroll 1
         for (int i0 = 4 * tid; i0 < n; i0 += 4 * kBatch * kEvictThreads) {
-            uint4 k[kBatch];
+            float4 v[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
-                k[u] = load4(i0 + 4 * u * kEvictThreads);
+                v[u] = mass4(i0 + 4 * u * kEvictThreads);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int i = i0 + 4 * u * kEvictThreads;
                 if (i >= n)
                     break;
+                const uint32_t x[4] = {mass_key(v[u].x), mass_key(v[u].y), mass_key(v[u].z),
+                                       mass_key(v[u].w)};
                 if constexpr (SMEM)
-                    *reinterpret_cast<uint4 *>(keys + i) = k[u];
+                    *reinterpret_cast<uint4 *>(keys + i) = make_uint4(x[0], x[1], x[2], x[3]);
                 if (i >= a && i + 4 <= z) {
-                    atomicAdd(mine + (k[u].x >> 21), 1u);
-                    atomicAdd(mine + (k[u].y >> 21), 1u);
-                    atomicAdd(mine + (k[u].z >> 21), 1u);
-                    atomicAdd(mine + (k[u].w >> 21), 1u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        atomicAdd(mine + (x[e] >> 21), 1u);
                 } else {
-                    const uint32_t x[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (i + e >= a && i + e < z)
@@ -260,22 +271,25 @@ __global__ void __launch_bounds__(kEvictThreads)
             sh.hist[1][i] = 0; // (for the second digit)
         }
         // counts of the keys whose bits from `above` up are `prefix`, by their bits from `shift`
-        auto count = [&](uint32_t *hist, uint32_t prefix, int above, int shift, uint32_t mask) {
-#pragma unroll 2
+        auto count = [&](uint32_t *hist, uint32_t prefix, int above, int shift) {
+            const uint32_t from = prefix << above, width = 1u << above;
+#pragma unroll 4
             for (int i = 4 * tid; i < z; i += 4 * kEvictThreads) {
                 const uint4 k = keys4(i);
-                const uint32_t x[4] = {k.x, k.y, k.z, k.w};
+                const uint32_t x[4] = {k.x - from, k.y - from, k.z - from, k.w - from};
+                if (min(min(x[0], x[1]), min(x[2], x[3])) < width) { // (few: one digit's keys)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if ((x[e] >> above) == prefix && i + e >= a && i + e < z)
-                        atomicAdd(hist + ((x[e] >> shift) & mask), 1u);
+                    for (int e = 0; e < 4; ++e)
+                        if (x[e] < width && i + e >= a && i + e < z)
+                            atomicAdd(hist + (x[e] >> shift), 1u);
+                }
             }
         };
         cluster_barrier(cluster, cs);
         pick_digit(cluster, sh, 0, 2048, wanted, tid, cs);
         uint32_t prefix = sh.digit;
         wanted = sh.rest;
-        count(sh.hist[1], prefix, 21, 10, 2047u);
+        count(sh.hist[1], prefix, 21, 10);
         // (every block is past its reads of the first counts, whose place the third ones take,
         // once it has come to this barrier: they are cleared after it)
         cluster_barrier(cluster, cs);
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kEvictThreads)
         for (int i = tid; i < 1024; i += kEvictThreads)
             sh.hist[0][i] = 0;
         __syncthreads();
-        count(sh.hist[0], prefix, 10, 0, 1023u);
+        count(sh.hist[0], prefix, 10, 0);
         cluster_barrier(cluster, cs);
         pick_digit(cluster, sh, 0, 1024, wanted, tid, cs);
         T = (prefix << 10) | sh.digit;
@@ -359,10 +373,13 @@ __global__ void __launch_bounds__(kEvictThreads)
             eq_before += te[r];
         }
     }
-#pragma unroll 1
+#pragma unroll 2
     for (int c = c0; c < c1; ++c) {
         const int i = c * 128 + 4 * lane;
         const uint32_t m = mark(i);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (m) // (the masses themselves: a key has lost NaN and the sign of zero)
+            x = mass4(i);
         // counts of the lanes before this one: above in the low half, equal in the high one
         const uint32_t own = __popc(m & 15u) | (__popc(m >> 4) << 16);
         uint32_t incl = own;
@@ -373,20 +390,22 @@ __global__ void __launch_bounds__(kEvictThreads)
                 incl += t;
         }
         const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-        uint32_t g = gt_before + ((incl - own) & 0xffffu), e = eq_before + ((incl - own) >> 16);
-        if (m) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool gt = (m >> u) & 1u, eq = (m >> (4 + u)) & 1u;
-                if (gt || (eq && e < ties)) {
-                    const uint32_t pos = g + (e < ties ? e : ties);
-                    kept[pos] = lo + i + u;
-                    new_mass[pos] = __ldg(src + i + u);
-                }
-                g += gt ? 1u : 0u;
-                e += eq ? 1u : 0u;
-            }
+        const uint32_t e = eq_before + ((incl - own) >> 16);
+        uint32_t pos = gt_before + ((incl - own) & 0xffffu) + min(e, ties);
+        // of those equal to the threshold, the first `ties` stay
+        uint32_t take = m & 15u, eq = m >> 4;
+        for (uint32_t k = e; eq && k < ties; ++k) {
+            take |= eq & (0u - eq);
+            eq &= eq - 1u;
         }
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if ((take >> u) & 1u) {
+                kept[pos] = lo + i + u;
+                new_mass[pos] = v[u];
+                ++pos;
+            }
         gt_before += all & 0xffffu;
         eq_before += all >> 16;
     }
