@@ -41,10 +41,20 @@ q8kv_status launch_verify(const VerifyParams &p, int B, int sms, cudaStream_t st
     // 16-byte loads where every row starts on 16 bytes
     const bool vec = aligned16(p.target) && p.target_stride % kVec == 0 &&
                      (!p.draft || (aligned16(p.draft) && p.draft_stride % kVec == 0));
-    // blocks per sequence: as many as one wave holds (4 blocks per SM)
-    int cs = kVerifyCluster;
-    while (cs > 1 && (long long)B * cs > 4LL * sms)
-        cs /= 2;
+    // Blocks per sequence: the fewest "waves times time of a block", where a wave holds 4 blocks
+    // per SM and a block takes its share of the row plus the time of about 8192 weights (start,
+    // accept test, exchange, search). 128 rows of 131075: 4 blocks; 600 rows: 4, not 1 (600
+    // blocks are a wave of 592 and one of 8: 112 us against 91).
+    const long long slots = 4LL * sms;
+    int cs = 1;
+    long long best = 0;
+    for (int c = 1; c <= kVerifyCluster; c *= 2) {
+        const long long cost = ((long long)B * c + slots - 1) / slots * (8192 + p.vocab / c);
+        if (c == 1 || cost <= best) {
+            best = cost;
+            cs = c;
+        }
+    }
     return vec ? launch_cluster(verify_kernel<T, kVec>, p, (unsigned)B, cs, kVerifyThreads, 0,
                                 stream)
                : launch_cluster(verify_kernel<T, 1>, p, (unsigned)B, cs, kVerifyThreads, 0, stream);
