@@ -15,8 +15,9 @@
 // bytes; a separate rotation would write and read the keys once more. A block takes a tile of
 // up to 4 tokens: the tile's cosines and sines are gathered into shared memory (one thread per
 // pair, whatever its axis; positions two tiles ahead, table entries one tile ahead by cp.async),
-// and its warps stream the tile's rows, 4 (or 2) rows of 8 (16) lanes at once as in the cache
-// write, each warp with the next rows in flight. Neighbouring warps take neighbouring rows,
+// and its warps stream the tile's rows, D / 16 lanes a row and 16 elements a lane, each warp with
+// the next rows in flight. A lane's four chunks of 4 elements lie D / 4 apart, so both members
+// of a pair are in one lane where rotary_dim is D or D / 2; other widths load the partner too. Neighbouring warps take neighbouring rows,
 // so the block reads and writes contiguous memory. (A first
 // version gave a warp one token and kept its angles in registers: 24 warps per SM at distant
 // addresses, waiting on every token's position -> table chain, ran the 32768-token fp32 prompt
@@ -32,9 +33,20 @@ namespace q8kv {
 constexpr unsigned kErrPosition = 0x40u; // a position outside the table (clamped)
 constexpr int kRopeAxes = 4;
 
-// How a pair's two channels lie: both in one lane (rotary_dim = head_dim), anywhere in the
-// row (a second load fetches the partner), or next to each other.
-enum RopeMode { kRopeFull = 0, kRopeHalf = 1, kRopeAdjacent = 2 };
+// How a pair's two channels lie: two chunks of a lane apart (rotary_dim = head_dim), one chunk
+// apart (head_dim / 2), anywhere in the row (a second load fetches the partner), or next to
+// each other.
+enum RopeMode { kRopeFull = 0, kRopeHalf = 1, kRopeAnywhere = 2, kRopeAdjacent = 3 };
+
+constexpr int kRopeChunks = 4; // chunks of 4 elements per lane and row
+__host__ __device__ constexpr int rope_lanes(int D)
+{
+    return D / 16; // lanes per row
+}
+__host__ __device__ constexpr int rope_rows(int D)
+{
+    return 32 / rope_lanes(D); // rows per warp and iteration
+}
 
 struct RopeParams {
     float *q_out;
@@ -111,24 +123,26 @@ __device__ __forceinline__ float4 rot_hi4(float4 b, float4 a, float4 c, float4 s
                        rot_hi(b.z, a.z, c.z, s.z), rot_hi(b.w, a.w, c.w, s.w));
 }
 
-// One row as loaded by its lanes: its chunks and, for kRopeHalf, the chunks of their partners.
-template <int D, typename T, int MODE>
+// One row as loaded by its lanes: its chunks and, for kRopeAnywhere, those of their partners.
+template <typename T, int MODE>
 struct RopeRow {
-    static constexpr int C = RowFrag<D>::C;
-    Raw4<T> x[C];
-    Raw4<T> y[MODE == kRopeHalf ? C : 1];
+    Raw4<T> x[kRopeChunks];
+    Raw4<T> y[MODE == kRopeAnywhere ? kRopeChunks : 1];
+};
+
+struct RopeFrag {
+    float4 x[kRopeChunks];
 };
 
 template <int D, typename T, int MODE>
-__device__ __forceinline__ RopeRow<D, T, MODE> load_row(const T *row, int sub, int rot, bool turn)
+__device__ __forceinline__ RopeRow<T, MODE> load_row(const T *row, int sub, int rot, bool turn)
 {
-    constexpr int LPR = write_lanes_per_row(D);
-    RopeRow<D, T, MODE> r;
+    RopeRow<T, MODE> r;
 #pragma unroll
-    for (int c = 0; c < RowFrag<D>::C; ++c) {
-        const int e = 4 * (sub + LPR * c);
+    for (int c = 0; c < kRopeChunks; ++c) {
+        const int e = 4 * (sub + rope_lanes(D) * c);
         r.x[c] = load_raw<T>(row + e);
-        if constexpr (MODE == kRopeHalf) {
+        if constexpr (MODE == kRopeAnywhere) {
             const int half = rot >> 1;
             r.y[c] = r.x[c];
             if (turn && e < rot)
@@ -138,47 +152,46 @@ __device__ __forceinline__ RopeRow<D, T, MODE> load_row(const T *row, int sub, i
     return r;
 }
 
-// The rotated row; cosines and sines of the token's pairs lie at cs and cs + half.
+// The rotated row; cosines of the token's pairs lie at cs, sines at cs + rot / 2.
 template <int D, typename T, int MODE>
-__device__ __forceinline__ RowFrag<D> rotate(const RopeRow<D, T, MODE> &r, const float *cs, int sub,
-                                             int rot, bool turn)
+__device__ __forceinline__ RopeFrag rotate(const RopeRow<T, MODE> &r, const float *cs, int sub,
+                                           int rot, bool turn)
 {
-    constexpr int LPR = write_lanes_per_row(D);
-    constexpr int C = RowFrag<D>::C;
-    RowFrag<D> f;
+    RopeFrag f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < kRopeChunks; ++c)
         f.x[c] = widen<T>(r.x[c]);
     if (!turn)
         return f;
-    const float *sn = cs + (rot >> 1);
-    if constexpr (MODE == kRopeFull) {
+    if constexpr (MODE == kRopeFull || MODE == kRopeHalf) {
+        constexpr int kApart = MODE == kRopeFull ? 2 : 1, kPairs = D / 4 * kApart;
 #pragma unroll
-        for (int c = 0; c < C / 2; ++c) {
-            const int e = 4 * (sub + LPR * c);
+        for (int c = 0; c < kApart; ++c) {
+            const int e = 4 * (sub + rope_lanes(D) * c);
             const float4 co = *reinterpret_cast<const float4 *>(cs + e);
-            const float4 si = *reinterpret_cast<const float4 *>(cs + D / 2 + e);
-            const float4 lo = f.x[c], hi = f.x[c + C / 2];
+            const float4 si = *reinterpret_cast<const float4 *>(cs + kPairs + e);
+            const float4 lo = f.x[c], hi = f.x[c + kApart];
             f.x[c] = rot_lo4(lo, hi, co, si);
-            f.x[c + C / 2] = rot_hi4(hi, lo, co, si);
+            f.x[c + kApart] = rot_hi4(hi, lo, co, si);
         }
-    } else if constexpr (MODE == kRopeHalf) {
+    } else if constexpr (MODE == kRopeAnywhere) {
         const int half = rot >> 1;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = 4 * (sub + LPR * c);
+        for (int c = 0; c < kRopeChunks; ++c) {
+            const int e = 4 * (sub + rope_lanes(D) * c);
             if (e >= rot)
                 continue;
             const bool low = e < half;
             const float4 y = widen<T>(r.y[c]);
             const float4 co = *reinterpret_cast<const float4 *>(cs + (low ? e : e - half));
-            const float4 si = *reinterpret_cast<const float4 *>(sn + (low ? e : e - half));
+            const float4 si = *reinterpret_cast<const float4 *>(cs + (low ? e + half : e));
             f.x[c] = low ? rot_lo4(f.x[c], y, co, si) : rot_hi4(f.x[c], y, co, si);
         }
     } else {
+        const float *sn = cs + (rot >> 1);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = 4 * (sub + LPR * c);
+        for (int c = 0; c < kRopeChunks; ++c) {
+            const int e = 4 * (sub + rope_lanes(D) * c);
             if (e >= rot)
                 continue;
             const float4 x = f.x[c];
@@ -191,10 +204,50 @@ __device__ __forceinline__ RowFrag<D> rotate(const RopeRow<D, T, MODE> &r, const
     return f;
 }
 
-// Iterations of a token: its query rows PPW at a time, then its key and value rows.
+// Quantise one row by the cache write's rule (q8kv_cache_write.cuh) with this kernel's lanes
+// (all of the warp take part in the reductions); if `store`, write the lane's codes. Returns
+// the row's scale and sets `bad` for a non-finite row.
+template <int D>
+__device__ __forceinline__ float rope_quantise(const RopeFrag &f, int8_t *dst, bool store, int sub,
+                                               bool &bad)
+{
+    float m = 0.f;
+    unsigned odd = 0;
+#pragma unroll
+    for (int c = 0; c < kRopeChunks; ++c) {
+        const float a[4] = {fabsf(f.x[c].x), fabsf(f.x[c].y), fabsf(f.x[c].z), fabsf(f.x[c].w)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            odd |= a[i] <= 3.402823466e38f ? 0u : 1u; // an infinity or a NaN
+            m = fmaxf(m, a[i]);
+        }
+    }
+#pragma unroll
+    for (int o = rope_lanes(D) / 2; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        odd |= __shfl_xor_sync(0xffffffffu, odd, o);
+    }
+    bad = odd != 0u;
+    if (m < 1e-6f)
+        m = 1.0f;
+    const float scale = bad ? __int_as_float(0x7fc00000) : __fmul_rn(m, 0x1.020408p-7f);
+    const float inv = __fdiv_rn(127.0f, m);
+    if (store) {
+#pragma unroll
+        for (int c = 0; c < kRopeChunks; ++c) {
+            const float4 x = f.x[c];
+            const uint32_t w = code_byte(x.x, inv) | (code_byte(x.y, inv) << 8) |
+                               (code_byte(x.z, inv) << 16) | (code_byte(x.w, inv) << 24);
+            reinterpret_cast<uint32_t *>(dst)[sub + rope_lanes(D) * c] = bad ? 0u : w;
+        }
+    }
+    return scale;
+}
+
+// Iterations of a token: its query rows, rope_rows(D) at a time, then its key and value rows.
 __host__ __device__ constexpr int rope_iters(int Hq, int Hk, int D)
 {
-    const int ppw = write_pairs_per_warp(D);
+    const int ppw = rope_rows(D);
     return (Hq + ppw - 1) / ppw + (2 * Hk + ppw - 1) / ppw;
 }
 
@@ -210,9 +263,9 @@ template <int D, typename T, int MODE>
 __global__ void __launch_bounds__(kWriteThreads, 3)
     rope_cache_write_kernel(const __grid_constant__ RopeParams p)
 {
-    constexpr int LPR = write_lanes_per_row(D);
-    constexpr int PPW = write_pairs_per_warp(D);
-    constexpr int C = RowFrag<D>::C;
+    constexpr int LPR = rope_lanes(D);
+    constexpr int PPW = rope_rows(D);
+    constexpr int C = kRopeChunks;
     __shared__ __align__(16) float angle[2][kRopeTile][D]; // cosines, then sines, of a token
     __shared__ long long tile_slot[2][kRopeTile];
     // the new rows may come from the kernel before this one on the stream
@@ -309,7 +362,7 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
         return;
     RopeUnit u = unit_at(unit);
     bool exists = false, turn = false;
-    RopeRow<D, T, MODE> cur;
+    RopeRow<T, MODE> cur;
     int tk = u.j / iters, it = u.j - tk * iters;
     if (u.j < u.j1)
         cur = load_row<D, T, MODE>(row_of(u.tok0 + tk, it, exists, turn), sub, p.rot, turn);
@@ -351,13 +404,13 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
                 load = true;
             }
             bool next_exists = false, next_turn = false;
-            RopeRow<D, T, MODE> next = cur;
+            RopeRow<T, MODE> next = cur;
             if (load)
                 next = load_row<D, T, MODE>(row_of(ntok, it, next_exists, next_turn), sub, p.rot,
                                             next_turn);
-            const RowFrag<D> f = rotate<D, T, MODE>(cur, angle[buf][t], sub, p.rot, turn);
+            const RopeFrag f = rotate<D, T, MODE>(cur, angle[buf][t], sub, p.rot, turn);
             if (i < q_iters) {
-                if constexpr (MODE == kRopeHalf)
+                if constexpr (MODE == kRopeAnywhere)
                     __syncwarp(); // in place: every lane has read its partners
                 if (exists) {
                     float4 *dst =
@@ -373,7 +426,7 @@ __global__ void __launch_bounds__(kWriteThreads, 3)
                 const long long row = store ? sl * p.Hk + (turn ? r : r - p.Hk) : 0;
                 bool bad;
                 const float sc =
-                    quantise_row<D>(f, (turn ? p.k : p.v) + row * D, store, sub, bad);
+                    rope_quantise<D>(f, (turn ? p.k : p.v) + row * D, store, sub, bad);
                 if (store) {
                     if (sub == 0)
                         (turn ? p.ks : p.vs)[row] = sc;

@@ -51,6 +51,9 @@ q8kv_status launch_rope(RopeParams &p, int mode, int sms, cudaStream_t stream)
     if (mode == kRopeHalf)
         return launch_pdl(rope_cache_write_kernel<D, T, kRopeHalf>, p, grid, kWriteThreads, 0,
                           stream);
+    if (mode == kRopeAnywhere)
+        return launch_pdl(rope_cache_write_kernel<D, T, kRopeAnywhere>, p, grid, kWriteThreads, 0,
+                          stream);
     return launch_pdl(rope_cache_write_kernel<D, T, kRopeAdjacent>, p, grid, kWriteThreads, 0,
                       stream);
 }
@@ -153,7 +156,10 @@ q8kv_status q8kv_rope_cache_write(float *q_out, int8_t *k_blocks, int8_t *v_bloc
     p.errors = dev->errors;
     if (pair_axis)
         std::memcpy(p.axis, pair_axis, (size_t)rotary_dim / 2);
-    const int mode = adjacent ? kRopeAdjacent : (rotary_dim == head_dim ? kRopeFull : kRopeHalf);
+    const int mode = adjacent                     ? kRopeAdjacent
+                     : rotary_dim == head_dim     ? kRopeFull
+                     : 2 * rotary_dim == head_dim ? kRopeHalf
+                                                  : kRopeAnywhere;
     if (dtype == Q8KV_F32)
         return launch_rope<float>(p, head_dim, mode, dev->sms, stream);
     if (dtype == Q8KV_F16)
