@@ -34,11 +34,24 @@ q8kv_status launch_pdl(void (*fn)(Params), const Params &p, unsigned grid, unsig
 template <int D, typename T>
 q8kv_status launch_rope(RopeParams &p, int mode, int sms, cudaStream_t stream)
 {
-    // Four tokens per block step when they fill a wave (3 blocks per SM), else one; a tile that
-    // still leaves SMs empty is shared by several blocks, of at least one row group per warp.
+    // Tokens per block step: the tile of 1 to 4 whose rounds over the wave of resident blocks take
+    // least, a round costing its tokens and about a third of one (4999 bf16 tokens: 3, not 4
+    // with a third round for 66 of 1250 tiles). A tile that leaves SMs empty is shared by
+    // several blocks, of at least one row group per warp.
     const int iters = rope_iters(p.Hq, p.Hk, D);
-    const long long wave = 3LL * sms;
-    p.tile = p.n_tokens >= kRopeTile * wave ? kRopeTile : 1;
+    const long long wave = (long long)rope_blocks<T>() * sms;
+    p.tile = 1;
+    long long least = 0;
+    for (int t = 1; t <= kRopeTile; ++t) {
+        const long long rounds = ((p.n_tokens + t - 1) / t + wave - 1) / wave;
+        const long long cost = rounds * (3 * t + 1);
+        if (t == 1 || cost <= least) {
+            least = cost;
+            p.tile = t;
+        }
+    }
+    if (p.n_tokens <= wave)
+        p.tile = 1;
     const long long tiles = (p.n_tokens + p.tile - 1) / p.tile;
     const long long most = (iters * p.tile + kWriteWarps - 1) / kWriteWarps;
     const long long parts = (wave + tiles - 1) / tiles;
