@@ -62,9 +62,9 @@ __device__ __forceinline__ float as_f32(__nv_bfloat16 x)
     return __bfloat162float(x);
 }
 
-// VEC consecutive elements: one 16-byte load, or a single element.
+// VEC consecutive elements by one load: 16 bytes, or as many as the rows' starts allow.
 template <typename T, int VEC>
-struct Pack {
+struct alignas(VEC * sizeof(T)) Pack {
     T v[VEC];
 };
 
@@ -72,12 +72,15 @@ template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
 {
     Pack<T, VEC> r;
-    if constexpr (VEC == 1) {
+    static_assert(VEC * sizeof(T) <= 16, "one load");
+    if constexpr (VEC == 1)
         r.v[0] = *p;
-    } else {
-        static_assert(VEC * sizeof(T) == 16, "one 16-byte load");
+    else if constexpr (VEC * sizeof(T) == 16)
         *reinterpret_cast<uint4 *>(r.v) = __ldg(reinterpret_cast<const uint4 *>(p));
-    }
+    else if constexpr (VEC * sizeof(T) == 8)
+        *reinterpret_cast<uint2 *>(r.v) = __ldg(reinterpret_cast<const uint2 *>(p));
+    else
+        *reinterpret_cast<uint32_t *>(r.v) = __ldg(reinterpret_cast<const uint32_t *>(p));
     return r;
 }
 
@@ -150,7 +153,8 @@ template <typename T, int VEC, int MODE>
 __device__ __forceinline__ double piece_sum_mode(const T *pr, const T *qr, int without, int lo,
                                                  int hi, int lane)
 {
-    constexpr int U = VEC == 1 ? 8 : (VEC == 4 ? 4 : 2); // packs of each row in flight per lane
+    // packs of each row in flight per lane
+    constexpr int U = VEC <= 2 ? 8 : (VEC == 4 ? 4 : 2);
     constexpr int kStep = 32 * VEC;
     double acc[2] = {0.0, 0.0};
     float err[2] = {0.f, 0.f};

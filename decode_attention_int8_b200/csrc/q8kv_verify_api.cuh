@@ -37,10 +37,15 @@ q8kv_status launch_cluster(void (*fn)(Params), const Params &p, unsigned cluster
 template <typename T>
 q8kv_status launch_verify(const VerifyParams &p, int B, int sms, cudaStream_t stream)
 {
+    // the widest load that every row's start allows: 16 bytes, two elements (an even vocabulary),
+    // or one
     constexpr int kVec = 16 / (int)sizeof(T);
-    // 16-byte loads where every row starts on 16 bytes
-    const bool vec = aligned16(p.target) && p.target_stride % kVec == 0 &&
-                     (!p.draft || (aligned16(p.draft) && p.draft_stride % kVec == 0));
+    auto starts = [&](int n) {
+        const uintptr_t bytes = (uintptr_t)n * sizeof(T);
+        return (reinterpret_cast<uintptr_t>(p.target) % bytes) == 0 && p.target_stride % n == 0 &&
+               (!p.draft || ((reinterpret_cast<uintptr_t>(p.draft) % bytes) == 0 &&
+                             p.draft_stride % n == 0));
+    };
     // Blocks per sequence: the fewest "waves times time of a block", where a wave holds 4 blocks
     // per SM and a block takes its share of the row plus the time of about 8192 weights (start,
     // accept test, exchange, search). 128 rows of 131075: 4 blocks; 600 rows: 4, not 1 (600
@@ -55,9 +60,11 @@ q8kv_status launch_verify(const VerifyParams &p, int B, int sms, cudaStream_t st
             cs = c;
         }
     }
-    return vec ? launch_cluster(verify_kernel<T, kVec>, p, (unsigned)B, cs, kVerifyThreads, 0,
-                                stream)
-               : launch_cluster(verify_kernel<T, 1>, p, (unsigned)B, cs, kVerifyThreads, 0, stream);
+    if (starts(kVec))
+        return launch_cluster(verify_kernel<T, kVec>, p, (unsigned)B, cs, kVerifyThreads, 0, stream);
+    if (starts(2))
+        return launch_cluster(verify_kernel<T, 2>, p, (unsigned)B, cs, kVerifyThreads, 0, stream);
+    return launch_cluster(verify_kernel<T, 1>, p, (unsigned)B, cs, kVerifyThreads, 0, stream);
 }
 
 } // namespace

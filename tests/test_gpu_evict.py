@@ -134,6 +134,20 @@ def test_a_sequence_within_budget_may_keep_its_blocks():
     assert err == 0
 
 
+@pytest.mark.parametrize("bs,L", [(7, 1000), (5, 20001), (1, 77), (33, 4099)])
+def test_rows_of_masses_that_start_anywhere(bs, L):
+    """Block sizes that leave the rows of mass unaligned: no 16-byte loads."""
+    check(2, 3, 64, bs, [L, L - 1], L // 3, 2, L // 9, seed=bs)
+
+
+@pytest.mark.parametrize("B,Hk,L", [(1, 1, 40000), (1, 2, 66000), (2, 4, 33000)])
+def test_clusters(B, Hk, L):
+    """Two, four and eight blocks per row, with ties on the threshold across blocks."""
+    def coarse(mass, *_):
+        mass[:] = np.round(mass * 50) / 50
+    check(B, Hk, 64, 64, [L] * B, 5000, 100, 900, seed=L, change=coarse)
+
+
 def test_twice_is_the_same():
     """Old blocks are read only: the same call again gives the same answer."""
     pools, mass, table, lens, new_table = make(2, 4, 128, 32, [700, 900], 300, seed=9)

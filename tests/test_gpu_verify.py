@@ -42,7 +42,7 @@ def draw(B, n, V, dtype, seed, spread=2.0, noise=0.7):
 
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("B,n,V", [(1, 4, 32000), (3, 0, 1000), (7, 1, 1), (5, 3, 2), (16, 5, 4099),
-                                   (2, 8, 65537), (64, 3, 777), (300, 2, 513), (700, 1, 64)])
+                                   (2, 8, 65537), (16, 4, 4098), (3, 5, 20006), (64, 3, 777), (300, 2, 513), (700, 1, 64)])
 def test_random_rows(dtype, B, n, V):
     target, draft, drafted, uni = draw(B, n, V, dtype, seed=B + V)
     a, t, err = call(target, draft, drafted, uni)
@@ -142,7 +142,7 @@ def test_strided_rows_and_unaligned_starts():
     """Rows inside a wider buffer, with strides and starts that 16-byte loads do not fit."""
     B, n, V = 5, 2, 1001
     target, draft, drafted, uni = draw(B, n, V, "fp32", seed=8)
-    for off, width in [(0, 1001), (0, 1004), (3, 1010), (4, 1024)]:
+    for off, width in [(0, 1001), (0, 1002), (2, 1006), (0, 1004), (3, 1010), (4, 1024)]:
         wt = torch.full((B, n + 1, width), 9.0, device="cuda")
         wd = torch.full((B, n, width), 9.0, device="cuda")
         if off + V > width:
