@@ -89,6 +89,8 @@ def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_ne
     sines; pair_axis: the axis of each of the rotary_dim / 2 pairs (a host sequence or bytes),
     None for one axis; adjacent: pairs (2p, 2p + 1) instead of (p, p + rotary_dim / 2)."""
     if pair_axis is not None:
+        if isinstance(pair_axis, int):  # (bytes(n) is n zeros)
+            raise TypeError("pair_axis must be a sequence of integers")
         pair_axis = bytes(pair_axis)
     status = (_native or native()).rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale,
                                                     q_new, k_new, v_new, slot_mapping, positions,

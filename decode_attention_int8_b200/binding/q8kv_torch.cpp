@@ -166,6 +166,8 @@ const void *token_rows(PyObject *o, const char *name, at::ScalarType type, int64
         refuse(t, name, s.str());
     }
     stride = n > 1 ? t.stride(0) : heads * D;
+    if (stride < heads * D && t.numel() > 0) // (an expanded token: the library's 0 means no gap)
+        refuse(t, name, "a token stride of at least " + std::to_string(heads * D));
     return t.data_ptr();
 }
 
@@ -178,7 +180,8 @@ const void *prob_rows(PyObject *o, const char *name, at::ScalarType type, int64_
               t.device() == dev && (vocab <= 1 || t.stride(2) == 1);
     if (ok) {
         stride = rows > 1 ? t.stride(1) : (B > 1 ? t.stride(0) : vocab);
-        ok = rows <= 1 || B <= 1 || t.stride(0) == rows * stride;
+        ok = (rows <= 1 || B <= 1 || t.stride(0) == rows * stride) &&
+             (stride >= vocab || t.numel() == 0); // (expanded rows: the library's 0 means no gap)
     }
     if (!ok) {
         std::ostringstream s;
@@ -360,6 +363,10 @@ PyObject *rope_cache_write(PyObject *, PyObject *const *a, Py_ssize_t n)
             axis = reinterpret_cast<const uint8_t *>(p);
         }
         const int adjacent = PyObject_IsTrue(a[12]);
+        if (adjacent < 0) {
+            PyErr_Clear();
+            throw Refused{PyExc_TypeError, "adjacent must be true or false"};
+        }
         const cudaStream_t st = stream_of(a[13], dev);
         const int size[9] = {whole(tokens, "tokens"), whole(axes, "axes"),
                              whole(Hq, "heads"),      whole(Hk, "heads"),

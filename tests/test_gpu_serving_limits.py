@@ -160,3 +160,43 @@ def test_binding_refusals_on_a_device():
         q8.q8kv_evict(**dict(ev, kept=z(1, 2, 17, dt=torch.int32)))
     torch.cuda.synchronize()
     assert q8.q8kv_device_errors(clear=True) == 0
+
+
+def test_expanded_rows_are_refused():
+    """A stride of zero (one row expanded over tokens or drafts) is not the library's zero, which
+    says that rows have no gap."""
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")
+    k, ks = z(4, 16, 2, 128, dt=torch.int8), z(4, 16, 2)
+    x, one = z(5, 2, 128), z(1, 2, 128).expand(5, 2, 128)
+    rope = dict(q_out=z(5, 2, 128), k_blocks=k, v_blocks=k.clone(), kscale=ks, vscale=ks.clone(),
+                q_new=x, k_new=x, v_new=x, slot_mapping=z(5, dt=torch.int64) - 1,
+                positions=z(1, 5, dt=torch.int32), cos_sin=z(8, 128))
+    for change in [dict(q_new=one), dict(k_new=one, v_new=one)]:
+        with pytest.raises(ValueError):
+            q8.q8kv_rope_cache_write(**dict(rope, **change))
+    ver = dict(n_accepted=z(2, dt=torch.int32), tokens=z(2, 3, dt=torch.int32),
+               target_probs=z(2, 3, 10), draft_probs=z(2, 2, 10),
+               draft_tokens=z(2, 2, dt=torch.int32), uniforms=z(2, 3))
+    for change in [dict(target_probs=z(1, 1, 10).expand(2, 3, 10)),
+                   dict(draft_probs=z(1, 1, 10).expand(2, 2, 10)),
+                   dict(target_probs=z(1, 3, 10).expand(2, 3, 10))]:
+        with pytest.raises(ValueError):
+            q8.q8kv_verify_draft(**dict(ver, **change))
+    ver = dict(ver, tokens=z(2, 1, dt=torch.int32), draft_probs=None, uniforms=z(2, 1),
+               draft_tokens=z(2, 0, dt=torch.int32))
+    with pytest.raises(ValueError):
+        q8.q8kv_verify_draft(**dict(ver, target_probs=z(1, 1, 10).expand(2, 1, 10)))
+    q8.q8kv_rope_cache_write(**rope)  # (the call that these differ from)
+    torch.cuda.synchronize()
+    assert q8.q8kv_device_errors(clear=True) == 0
+
+
+def test_options_of_the_wrong_kind_are_refused():
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")
+    k, ks, x = z(4, 16, 2, 128, dt=torch.int8), z(4, 16, 2), z(5, 2, 128)
+    rope = dict(q_out=z(5, 2, 128), k_blocks=k, v_blocks=k.clone(), kscale=ks, vscale=ks.clone(),
+                q_new=x, k_new=x, v_new=x, slot_mapping=z(5, dt=torch.int64) - 1,
+                positions=z(1, 5, dt=torch.int32), cos_sin=z(8, 128))
+    for change in [dict(pair_axis=64), dict(adjacent=torch.zeros(2)), dict(stream="first")]:
+        with pytest.raises(TypeError):
+            q8.q8kv_rope_cache_write(**dict(rope, **change))
