@@ -190,7 +190,15 @@ __device__ __forceinline__ double piece_sum_mode(const T *pr, const T *qr, int w
                 acc[i & 1] += weight<MODE>(as_f32(pr[e0 + i]),
                                            MODE == kResidual ? as_f32(qr[e0 + i]) : 0.f, e0 + i,
                                            without);
-    return warp_sum((acc[0] + acc[1]) + ((double)err[0] + (double)err[1]));
+    double sum = warp_sum((acc[0] + acc[1]) + ((double)err[0] + (double)err[1]));
+    if (!(sum < INFINITY)) { // weights near fp32's largest, whose pair overflows, or an infinity
+        sum = 0.0;
+#pragma unroll 1
+        for (int e = lo + lane; e < hi; e += 32)
+            sum += weight<MODE>(as_f32(pr[e]), MODE == kResidual ? as_f32(qr[e]) : 0.f, e, without);
+        sum = warp_sum(sum);
+    }
+    return sum;
 }
 
 template <typename T, int VEC>

@@ -482,7 +482,8 @@ q8kv_status q8kv_rope_cache_write(float *q_out, int8_t *k_blocks, int8_t *v_bloc
  *   n_accepted    int32 [B]
  *   tokens        int32 [B][max_drafts + 1]: the accepted drafts, the drawn token, then -1
  *   target_probs  dtype [B][max_drafts + 1] rows of vocab, target_stride elements apart
- *   draft_probs   dtype [B][max_drafts] rows, draft_stride elements apart; NULL for drafts
+ *   draft_probs   dtype [B][max_drafts] rows of weights >= 0, draft_stride elements apart; NULL for
+ *                 drafts
  *                 without probabilities (each is then certain: accepted while uniform <
  *                 target's, and a refusal draws from the target's row without the token)
  *   draft_tokens  int32 [B][max_drafts] (may be NULL when max_drafts is 0)

@@ -167,3 +167,23 @@ def test_draws_follow_the_target():
     n = np.bincount(t[:, 0], minlength=V)
     want = p.double().cpu().numpy() * B
     assert (np.abs(n - want) < 6 * np.sqrt(want) + 6).all() and err == 0
+
+
+@pytest.mark.parametrize("V", [7, 600, 1024, 5000, 65536])
+def test_weights_near_the_largest(V):
+    """Rows need not sum to one: weights of which two pass fp32's range still have an fp64 sum."""
+    target = torch.zeros((4, 2, V))
+    draft = torch.zeros((4, 1, V))
+    target[:, 0], target[:, 1] = 3e38, 2.5e38
+    target[0, 0, 0] = 1.0
+    draft[1] = 1e37
+    uni = torch.tensor([[0.5, 0.7], [0.5, 0.31], [0.0, 0.0], [0.5, 1 - 2.0 ** -24]])
+    drafted = torch.tensor([[0], [V], [0], [V - 1]]).int()
+    drafted[1] = 1
+    uni[1, 0] = 1.0
+    target[1, 0, 1] = 0.0  # refused: the residual of the others
+    target[3, 0, V - 1] = 0.0
+    for q in (draft, None):
+        a, t, err = call(target.cuda(), None if q is None else q.cuda(), drafted, uni)
+        ra, rt = ref.verify(host(target), host(q), drafted.numpy(), uni.numpy())
+        assert np.array_equal(a, ra) and np.array_equal(t, rt) and err == 0
