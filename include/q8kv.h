@@ -91,6 +91,9 @@ typedef enum {
 #define Q8KV_DEVERR_PROBS 0x80u      /* draft verification: a draft token or draft count out of
                                         range, or no probability to draw a token from         */
 
+/* The first call of an entry point on a device sets up (the error word's address, the kernels'
+ * attributes): make it before a stream capture begins. */
+
 /* Element type of rows that may come in several (q8kv_rope_cache_write, q8kv_verify_draft). */
 typedef enum { Q8KV_F32 = 0, Q8KV_F16 = 1, Q8KV_BF16 = 2 } q8kv_dtype;
 
@@ -482,10 +485,9 @@ q8kv_status q8kv_rope_cache_write(float *q_out, int8_t *k_blocks, int8_t *v_bloc
  *   n_accepted    int32 [B]
  *   tokens        int32 [B][max_drafts + 1]: the accepted drafts, the drawn token, then -1
  *   target_probs  dtype [B][max_drafts + 1] rows of vocab, target_stride elements apart
- *   draft_probs   dtype [B][max_drafts] rows of weights >= 0, draft_stride elements apart; NULL for
- *                 drafts
- *                 without probabilities (each is then certain: accepted while uniform <
- *                 target's, and a refusal draws from the target's row without the token)
+ *   draft_probs   dtype [B][max_drafts] rows of weights >= 0, draft_stride elements apart; NULL
+ *                 for drafts without probabilities (each is then certain: accepted while
+ *                 uniform < target's, and a refusal draws from the target's row without it)
  *   draft_tokens  int32 [B][max_drafts] (may be NULL when max_drafts is 0)
  *   n_drafts      int32 [B], or NULL: max_drafts each
  *   uniforms      fp32 [B][max_drafts + 1], in [0, 1)
