@@ -10,6 +10,33 @@ namespace {
 using namespace q8kv;
 
 bool g_evict_attr[kMaxDevices];
+int g_evict_clusters[kMaxDevices][4]; // clusters of 1 << i blocks, one block per SM, in one wave
+
+// Sets the kernels' attributes and counts the clusters that run at once (the SMs that share a
+// scheduler's cluster space need not be a multiple of the cluster's size).
+q8kv_status evict_setup(DeviceInfo *dev, int d)
+{
+    Q8KV_CUDA(cudaFuncSetAttribute(evict_select_kernel<true>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, dev->smem_optin));
+    Q8KV_CUDA(cudaFuncSetAttribute(evict_select_kernel<false>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, dev->smem_optin));
+    for (int i = 0; (1 << i) <= kEvictCluster; ++i) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1u << i);
+        cfg.blockDim = dim3(kEvictThreads);
+        cfg.dynamicSmemBytes = (size_t)dev->smem_optin;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        Q8KV_CUDA(cudaOccupancyMaxActiveClusters(&g_evict_clusters[d][i],
+                                                 evict_select_kernel<true>, &cfg));
+    }
+    g_evict_attr[d] = true;
+    return Q8KV_OK;
+}
 
 template <int D>
 q8kv_status launch_move(const EvictParams &p, cudaStream_t stream)
@@ -74,13 +101,9 @@ q8kv_status q8kv_evict(int8_t *k_blocks, int8_t *v_blocks, float *kscale, float 
             return st;
         const int d = (int)(dev - g_dev);
         if (!g_evict_attr[d]) {
-            Q8KV_CUDA(cudaFuncSetAttribute(evict_select_kernel<true>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           dev->smem_optin));
-            Q8KV_CUDA(cudaFuncSetAttribute(evict_select_kernel<false>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           dev->smem_optin));
-            g_evict_attr[d] = true;
+            st = evict_setup(dev, d);
+            if (st != Q8KV_OK)
+                return st;
         }
     }
     p.mass = mass;
@@ -108,10 +131,14 @@ q8kv_status q8kv_evict(int8_t *k_blocks, int8_t *v_blocks, float *kscale, float 
     p.new_cap = new_max_blocks_per_seq * kv_block_size;
     p.errors = dev->errors;
     // Blocks per (sequence, head): one for up to 16 masses per thread, more for longer rows
-    // while the machine has room for them (a block per SM).
+    // while all clusters run at once, a block per SM (18 rows of 140000 masses: clusters of 4,
+    // 49.5 us with the move; of 8 they take two rounds, 63.2 us. 14 rows: 8, 37.7 us. Rows of
+    // 16384 in 32 pairs: one block each 28.8 us, clusters of 2 32.3 us, whose barriers cost more
+    // than the shares save).
     const long long pairs = (long long)B * n_kv_heads;
+    const int *at_once = g_evict_clusters[dev - g_dev];
     int cs = 1;
-    while (cs < kEvictCluster && pairs * cs * 2 <= dev->sms && p.cap > 16 * kEvictThreads * cs)
+    for (int i = 1; cs < kEvictCluster && pairs <= at_once[i] && p.cap > 16 * kEvictThreads * cs; ++i)
         cs *= 2;
     // and as many as it takes for a block's masses to fit its shared memory
     auto part = [&](int n) { return ((size_t)((p.cap + n - 1) / n + 31) & ~(size_t)31) * 4; };

@@ -148,6 +148,14 @@ def test_clusters(B, Hk, L):
     check(B, Hk, 64, 64, [L] * B, 5000, 100, 900, seed=L, change=coarse)
 
 
+@pytest.mark.parametrize("B,L", [(14, 70000), (18, 70000), (40, 34000), (80, 17000)])
+def test_as_many_clusters_as_run_at_once(B, L):
+    """Around the numbers of rows from which a row gets fewer blocks."""
+    rng = np.random.default_rng(B)
+    lens = [L] + (L - rng.integers(0, L // 4, B - 1)).tolist()
+    check(B, 1, 64, 64, lens, 300, 10, 100, seed=B, spare=1)
+
+
 def test_twice_is_the_same():
     """Old blocks are read only: the same call again gives the same answer."""
     pools, mass, table, lens, new_table = make(2, 4, 128, 32, [700, 900], 300, seed=9)
