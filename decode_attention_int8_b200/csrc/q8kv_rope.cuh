@@ -17,11 +17,12 @@
 // pair, whatever its axis; positions two tiles ahead, table entries one tile ahead by cp.async),
 // and its warps stream the tile's rows, D / 16 lanes a row and 16 elements a lane, each warp with
 // the next rows in flight. A lane's four chunks of 4 elements lie D / 4 apart, so both members
-// of a pair are in one lane where rotary_dim is D or D / 2; other widths load the partner too. Neighbouring warps take neighbouring rows,
-// so the block reads and writes contiguous memory. (A first
-// version gave a warp one token and kept its angles in registers: 24 warps per SM at distant
-// addresses, waiting on every token's position -> table chain, ran the 32768-token fp32 prompt
-// in 632 us.) Few tokens leave SMs empty, so a tile's rows are then split over several blocks.
+// of a pair are in one lane where rotary_dim is D or D / 2; other widths load the partner too.
+// Neighbouring warps take neighbouring rows, so the block reads and writes contiguous memory.
+// (A first version gave a warp one token and kept its angles in registers: 24 warps per SM at
+// distant addresses, waiting on every token's position -> table chain, ran the 32768-token fp32
+// prompt in 632 us, this one in 229, 0.95 of the copy rate.) Few tokens leave SMs empty, so a
+// tile's rows are then split over several blocks.
 #pragma once
 
 #include <cuda_bf16.h>

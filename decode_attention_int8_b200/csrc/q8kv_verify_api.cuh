@@ -48,8 +48,9 @@ q8kv_status launch_verify(const VerifyParams &p, int B, int sms, cudaStream_t st
     };
     // Blocks per sequence: the fewest "waves times time of a block", where a wave holds 4 blocks
     // per SM and a block takes its share of the row plus the time of about 8192 weights (start,
-    // accept test, exchange, search). 128 rows of 131075: 4 blocks; 600 rows: 4, not 1 (600
-    // blocks are a wave of 592 and one of 8: 112 us against 91).
+    // accept test, exchange, search). Measured, fp32, 5 drafts, with 1 / 2 / 4 / 8 blocks: 128 rows
+    // of 131075 57 / 36 / 29 / 32 us; 600 of them (a wave of 592 and one of 8, with one block
+    // each) 129 / 111 / 108 / 120; 32 rows 50 / 29 / - / 13; 600 rows of 32000 42 / 39 / - / 68.
     const long long slots = 4LL * sms;
     int cs = 1;
     long long best = 0;
