@@ -30,7 +30,9 @@ q8kv_status launch_mass(const MassParams &p, DeviceInfo *dev, int warps, cudaStr
     long long wave = (long long)(dev->smem_optin / (smem + 1024));
     wave = (wave < 1 ? 1 : (wave > 3 ? 3 : wave)) * dev->sms;
     const long long tiles = (long long)p.B * ((p.cap + kMassTile - 1) / kMassTile);
-    return launch_pdl(attn_mass_kernel<MODE>, p, (unsigned)(tiles < wave ? tiles : wave),
+    const long long shares = wave / p.passes > 1 ? wave / p.passes : 1; // of the tokens
+    return launch_pdl(attn_mass_kernel<MODE>, p,
+                      (unsigned)((tiles < shares ? tiles : shares) * p.passes),
                       (unsigned)warps * 32u, smem, stream);
 }
 
@@ -93,13 +95,18 @@ q8kv_status q8kv_attn_mass(float *mass, const float *q, const float *lse, const 
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.decay = decay;
     p.errors = dev->errors;
-    // Up to 8 warps: the heads in the fewest even passes (a pass holds the query rows of its
-    // heads, at most 256 of them, in shared memory), the tokens split over the warps left.
+    // Up to 8 warps: a few heads' worth, the tokens split over the warps left; other blocks take
+    // the other heads of the same tokens. A block quantises its heads' query rows at the start
+    // of every sequence, so with many rows, or few tokens, fewer heads (us with 8 / 4 / 2 / 1):
+    //   16 x 4096, 8 heads of 4 rows      17.3 / 16.9 / 17.4 / 17.7    256 x 100: 12.6 / 12.6 / 14.5 / 19.1
+    //   16 x 500, 8 heads of 8 rows        7.9 /  7.3 /  6.8 /  7.6    1 x 256:    4.8 /  3.9 /  3.6 /  3.5
+    //   24 x 8192, 8 heads of 32 rows     82.6 / 74.4 / 73.9 / 71.0    2 x 2388:  17.8 / 11.7 /  8.6 /  7.6
     p.rows = p.R <= 4 ? 4 : (p.R + 7) & ~7;
-    int most = 256 / p.rows;
-    most = most > kMassMaxWarps ? kMassMaxWarps : (most < 1 ? 1 : most);
+    const long long warp_tiles = (long long)B * (p.cap / kMassTile) * n_kv_heads;
+    const int most = p.rows > 8 ? 1 : (warp_tiles <= 2LL * 3 * kMassMaxWarps * dev->sms ? 2 : 4);
     const int passes = (n_kv_heads + most - 1) / most;
     p.heads_pass = (n_kv_heads + passes - 1) / passes;
+    p.passes = (n_kv_heads + p.heads_pass - 1) / p.heads_pass;
     p.subs = kMassMaxWarps / p.heads_pass;
     const int warps = p.heads_pass * p.subs;
     if (p.R <= 4)
