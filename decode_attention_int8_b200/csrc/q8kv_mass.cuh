@@ -8,8 +8,8 @@
 // the log-sum-exp of each row that the decode left: one pass over K, no softmax to redo.
 //
 // What bounds it: HBM, at 132 bytes of K and 8 of mass per (token, KV head), then the issue
-// slots (48 ragged sequences of up to 16384 tokens, 64 / 8 heads: 74 us, 0.83 of the copy rate;
-// 16 x 4096, 32 / 8: 18 us, 0.63, the rest its start). A warp takes 16 tokens of one head at a
+// slots (48 ragged sequences of up to 16384 tokens, 64 / 8 heads: 73 us, 0.85 of the copy rate;
+// 16 x 4096, 32 / 8: 17 us, 0.67, the rest its start). A warp takes 16 tokens of one head at a
 // time as the M rows of mma.m16n8k32.s8, query rows as its N columns:
 //  * 5 or more rows per head: eight rows per MMA, one MMA per 32-channel block, K fragments by
 //    ldmatrix.
