@@ -109,6 +109,12 @@ def test_mass_many_sequences_and_rows(B, nq, Hq, Hk):
     assert q8.q8kv_device_errors(clear=True) == 0
 
 
+@pytest.mark.parametrize("B,nq,Hq,Hk", [(2, 1, 500, 500), (3, 3, 520, 130), (5, 2, 26, 13)])
+def test_mass_many_heads(B, nq, Hq, Hk):
+    """More heads than blocks run at once, and numbers of heads that no block size divides."""
+    test_mass_many_sequences_and_rows(B, nq, Hq, Hk)
+
+
 def test_binding_refusals_on_a_device():
     """Shapes, types, devices and strides that disagree never reach the library."""
     z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")
