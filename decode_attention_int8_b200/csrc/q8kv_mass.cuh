@@ -487,7 +487,10 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
             last = at;
             at = at == (kMassStages - 1) * kMassStageBytes ? 0 : at + kMassStageBytes;
         }
+        // (a lane's own copies are done; the barrier is for the other lanes' reads of the last
+        // tiles, whose places the next segment's first copies take)
         asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
     }
 }
 
