@@ -281,11 +281,11 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
         // table, and quantised after.
         const int part = lane & 15; // block part / 4, its values 8 (part % 4) ..
         const int all_rows = p.heads_pass * p.rows;
-        float vs[kMassLoads][8], l2s[kMassLoads];
-        auto load_query = [&](int x, float (&v)[8], float &l2) {
+        float vs[kMassLoads][8], ls[kMassLoads];
+        auto load_query = [&](int x, float (&v)[8], float &l) {
             const int hd = MODE == kMassQuad ? x >> 2 : (MODE == kMassOct ? x >> 3 : x / p.rows);
             const int r = x - hd * p.rows;
-            l2 = INFINITY;
+            l = 3.402823466e38f; // no row: +inf in base 2, no weight
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = 0.f;
@@ -298,25 +298,36 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
                 const float4 y = __ldg(src), w = __ldg(src + 1);
                 v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
                 v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
-                l2 = __ldg(p.lse + row) * 1.44269504088896341f;
+                l = __ldg(p.lse + row);
             }
         };
         auto load_queries = [&](int x0) {
 #pragma unroll
             for (int i = 0; i < kMassLoads; ++i)
-                load_query(x0 + 2 * nwarps * i + (lane >> 4), vs[i], l2s[i]);
+                load_query(x0 + 2 * nwarps * i + (lane >> 4), vs[i], ls[i]);
         };
         load_queries(2 * warp);
 #pragma unroll
         for (int i = 0; i < kMassStages - 1; ++i)
             fetch(i * kMassStageBytes);
         __syncthreads(); // the last segment's rows have been read
-        auto put_query = [&](int x, const float (&v)[8], float l2) {
+        auto put_query = [&](int x, const float (&v)[8], float l) { // (whole warps)
             const int hd = MODE == kMassQuad ? x >> 2 : (MODE == kMassOct ? x >> 3 : x / p.rows);
             const int r = x - hd * p.rows;
             uint32_t lo, hi;
             float qsc;
             quantize_block_quad(v, lo, hi, qsc);
+            // A NaN channel would leave the codes as a zero (the quantiser's maximum and conversion
+            // drop it): the row's statistic takes it up instead, and with it every weight. (An
+            // infinity is the block's scale, under codes of 0: the scores are NaN by themselves.) A
+            // statistic of +inf would weigh nothing, like a row that is not there.
+            bool bad = l == INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                bad |= v[i] != v[i];
+            const float l2 = __ballot_sync(kFullMask, bad) & (0xffffu << (lane & 16))
+                                 ? __int_as_float(0x7fc00000)
+                                 : l * 1.44269504088896341f;
             if (x < all_rows) { // (the last step may pass the last row)
                 *reinterpret_cast<uint2 *>(msm + lay.off_codes +
                                            (uint32_t)(x * kMassRowBytes + 8 * part)) =
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(kMassMaxWarps * 32, 3)
 #pragma unroll
             for (int i = 0; i < kMassLoads; ++i)
                 if (x0 + 2 * nwarps * i < all_rows)
-                    put_query(x0 + 2 * nwarps * i + (lane >> 4), vs[i], l2s[i]);
+                    put_query(x0 + 2 * nwarps * i + (lane >> 4), vs[i], ls[i]);
             x0 += 2 * nwarps * kMassLoads;
             if (x0 >= all_rows)
                 break;

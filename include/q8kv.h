@@ -356,7 +356,10 @@ q8kv_status q8kv_quest_metadata(float *maxblocks, float *minblocks, const int8_t
  *              of at least q8kv_workspace_bytes(B, n_queries * n_q_heads, n_kv_heads,
  *              head_dim) bytes; calls that may overlap, two captured graphs among them, use
  *              one each.
- * Other arguments, shapes, errors and asynchrony as q8kv_decode_attn_multi.
+ * A NaN in a query row counts as zero, as in the other decode calls (it has no part in its block's
+ * maximum and its code is 0); an infinity gives lse NaN and an output without meaning.
+ * q8kv_attn_mass answers NaN for both. Other arguments, shapes, errors and asynchrony as
+ * q8kv_decode_attn_multi.
  */
 q8kv_status q8kv_decode_attn_lse(float *out, float *lse, const float *q, const int8_t *k_blocks,
                                  const int8_t *v_blocks, const float *kscale,
@@ -381,8 +384,9 @@ q8kv_status q8kv_decode_attn_lse(float *out, float *lse, const float *q, const i
  *   decay  in [0, 1]: 1 adds up, less forgets, 0 writes the weights without reading mass
  *   lse    fp32 [B][n_queries][n_q_heads]
  * Tokens of a block whose table entry is outside the pool keep their mass
- * (Q8KV_DEVERR_BLOCK_TABLE); a seq_len out of range is clamped (Q8KV_DEVERR_SEQ_LEN). A
- * non-finite query, scale or lse gives non-finite masses, as it gives non-finite outputs.
+ * (Q8KV_DEVERR_BLOCK_TABLE); a seq_len out of range is clamped (Q8KV_DEVERR_SEQ_LEN). A query
+ * row that holds an infinity or a NaN, or whose lse is NaN or +inf, gives NaN to every token that
+ * it sees, and a scale that is not finite gives its token a mass that is not.
  * Supported: head_dim 128; kv_block_size a power of two in [16, 256]; n_queries *
  * n_q_heads / n_kv_heads <= 128; n_kv_heads <= 4096; B <= 16384. One kernel launch, no
  * workspace, asynchronous on `stream`, programmatic dependent launch as the other kernels.
