@@ -9,8 +9,9 @@
 //
 // Products and sums carry fp64's precision. The answer is a whole number: a sum over 1e5 weights in
 // fp32 is off by about 1e-7 of Z, and with that many borders in [0, Z) one draw in a few
-// hundred would name a neighbour. With fp64 accumulators (and exact fp32 steps before them) the
-// sums' order moves a border by less than 1e-13 Z.
+// hundred would name a neighbour. With fp64 accumulators, and fp32 steps before them whose rounding
+// errors are summed up too, a border moves by less than 1e-13 Z, beside the roundings of the fp64
+// sums (2^-53 of the running sum for each of a lane's).
 //
 // What bounds it: HBM for large batches (one row of p, and one of q after a refusal, read
 // once), latency for small ones. A cluster of up to 8 blocks takes a sequence: every block
@@ -146,9 +147,12 @@ __device__ __forceinline__ float pair_sum(float a, float b, float &err)
 
 // Sum of the weights of tokens [lo, hi), one warp (lo a multiple of VEC). Two weights are added
 // up in fp32 first, exactly: their sum goes to the fp64 accumulator, and the rounding errors, at
-// most 2^-24 of it, to an fp32 one whose own errors are below 2^-45 of the total. That takes
-// half a conversion and half an fp64 sum per weight instead of two and two (128 rows of 131072
-// bf16 weights: 20.6 us, 23.2 us with fp64 differences; fp32: 25.7, 26.6).
+// most 2^-23 of it, to an fp32 one that is emptied into fp64 every turn. Its own errors are then
+// those of 13 sums of at most 2^-23 of the turn's weights each, so below 13 * 2^-47 = 2^-43.3 of the
+// total whatever the length. (Kept over the whole row, roundings of one sign put it off by 1e-12
+// of the total after 8192 weights of a lane.) That takes little more than half a conversion and half
+// an fp64 sum per weight instead of two and two (128 rows of 131072 bf16 weights: 20.6 us, 23.2
+// us with fp64 differences; fp32: 25.7, 26.6).
 template <typename T, int VEC, int MODE>
 __device__ __forceinline__ double piece_sum_mode(const T *pr, const T *qr, int without, int lo,
                                                  int hi, int lane)
@@ -157,11 +161,11 @@ __device__ __forceinline__ double piece_sum_mode(const T *pr, const T *qr, int w
     constexpr int U = VEC <= 2 ? 8 : (VEC == 4 ? 4 : 2);
     constexpr int kStep = 32 * VEC;
     double acc[2] = {0.0, 0.0};
-    float err[2] = {0.f, 0.f};
     int e0 = lo + lane * VEC;
 #pragma unroll 1
     for (; e0 + (U - 1) * kStep + VEC <= hi; e0 += U * kStep) { // (lanes may differ by one turn)
         Pack<T, VEC> a[U], b[U];
+        float err[2] = {0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             a[u] = load_pack<T, VEC>(pr + e0 + u * kStep);
@@ -181,6 +185,7 @@ __device__ __forceinline__ double piece_sum_mode(const T *pr, const T *qr, int w
             }
             acc[c] += (double)pair_sum(w[0], w[1], err[c]);
         }
+        acc[0] += (double)(err[0] + err[1]);
     }
 #pragma unroll 1
     for (; e0 < hi; e0 += kStep)
@@ -190,7 +195,7 @@ __device__ __forceinline__ double piece_sum_mode(const T *pr, const T *qr, int w
                 acc[i & 1] += weight<MODE>(as_f32(pr[e0 + i]),
                                            MODE == kResidual ? as_f32(qr[e0 + i]) : 0.f, e0 + i,
                                            without);
-    double sum = warp_sum((acc[0] + acc[1]) + ((double)err[0] + (double)err[1]));
+    double sum = warp_sum(acc[0] + acc[1]);
     if (!(sum < INFINITY)) { // weights near fp32's largest, whose pair overflows, or an infinity
         sum = 0.0;
 #pragma unroll 1
