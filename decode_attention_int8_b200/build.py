@@ -2,6 +2,7 @@
 half of its torch binding."""
 from __future__ import annotations
 
+import contextlib
 import glob
 import os
 import shutil
@@ -58,27 +59,48 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile binding/q8kv_torch.cpp against the running torch if it is stale."""
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "q8kv.h")]
-    if not force and os.path.exists(BINDING) and \
-            all(os.path.getmtime(BINDING) >= os.path.getmtime(d) for d in deps):
-        return BINDING
+def binding_command(out: str) -> list:
+    """The compile command of the binding, against the running torch and Python."""
     import torch
 
     torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    lib = os.path.join(torch_dir, "lib")
-    tmp = BINDING + ".tmp.%d" % os.getpid()
-    subprocess.check_call([
+    return [
         "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
         "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
         "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
         "-isystem", os.path.join(cuda, "include"),
         "-isystem", sysconfig.get_paths()["include"],
-        BINDING_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+        BINDING_SRC, "-o", out, "-L", os.path.join(torch_dir, "lib"),
+        "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile binding/q8kv_torch.cpp against the running torch if the module is stale: older than
+    its sources, or built against another torch, Python or by another command (the record of
+    that lies beside the module: one built against another torch may load, and read tensors by
+    an outdated layout)."""
+    import torch
+
+    record = BINDING + ".built"
+    # (of the command the flags: the folders may differ from one machine to the next)
+    flags = [f for f in binding_command(BINDING) if not os.path.isabs(f)]
+    against = "\n".join([torch.__version__, str(sysconfig.get_config_var("EXT_SUFFIX")), *flags])
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "q8kv.h")]
+    if not force and os.path.exists(BINDING) and os.path.exists(record) and \
+            all(os.path.getmtime(BINDING) >= os.path.getmtime(d) for d in deps):
+        with open(record) as f:
+            if f.read() == against:
+                return BINDING
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    subprocess.check_call(binding_command(tmp))
+    with contextlib.suppress(FileNotFoundError):  # (never the old record beside a new module)
+        os.remove(record)
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(against)
+    os.replace(tmp, record)
     return BINDING
 
 
