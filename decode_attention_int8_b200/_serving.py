@@ -13,6 +13,7 @@ does not fit raises ValueError (or TypeError), a refusal of the library Q8KVErro
 from __future__ import annotations
 
 import ctypes
+import operator
 import threading
 
 from . import _lib
@@ -89,8 +90,13 @@ def q8kv_rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale, q_new, k_ne
     sines; pair_axis: the axis of each of the rotary_dim / 2 pairs (a host sequence or bytes),
     None for one axis; adjacent: pairs (2p, 2p + 1) instead of (p, p + rotary_dim / 2)."""
     if pair_axis is not None:
-        if isinstance(pair_axis, int):  # (bytes(n) is n zeros)
-            raise TypeError("pair_axis must be a sequence of integers")
+        # bytes() of a count is that many zeros, and of an array its memory: only what holds one
+        # axis per entry goes there as it is
+        if not isinstance(pair_axis, (bytes, bytearray, list, tuple)):
+            try:
+                pair_axis = [operator.index(axis) for axis in pair_axis]
+            except TypeError:
+                raise TypeError("pair_axis must be a sequence of integers") from None
         pair_axis = bytes(pair_axis)
     status = (_native or native()).rope_cache_write(q_out, k_blocks, v_blocks, kscale, vscale,
                                                     q_new, k_new, v_new, slot_mapping, positions,
