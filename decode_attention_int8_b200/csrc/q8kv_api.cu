@@ -528,13 +528,14 @@ q8kv_status run(const Call &c, void *ws, size_t ws_bytes, bool managed_ws, cudaS
     if (managed_ws) {
         std::lock_guard<std::mutex> lock(g_mutex);
         if (dev->ws_bytes < pl.ws_bytes) {
-            if (dev->ws) {
-                Q8KV_CUDA(cudaFree(dev->ws));
-                dev->ws = nullptr;
-                dev->ws_bytes = 0;
-            }
-            Q8KV_CUDA(cudaMalloc(&dev->ws, pl.ws_bytes));
-            dev->ws_bytes = pl.ws_bytes;
+            // A smaller workspace stays allocated: a captured graph may hold its address and be
+            // replayed after this. Sizes at least double, so that what stays is less than the
+            // workspace in use (20 MB for the largest shape on 148 SMs).
+            const size_t bytes = pl.ws_bytes > 2 * dev->ws_bytes ? pl.ws_bytes : 2 * dev->ws_bytes;
+            void *ws_new = nullptr;
+            Q8KV_CUDA(cudaMalloc(&ws_new, bytes));
+            dev->ws = ws_new;
+            dev->ws_bytes = bytes;
         }
         ws = dev->ws;
         ws_bytes = dev->ws_bytes;

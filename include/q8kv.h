@@ -100,9 +100,10 @@ typedef enum { Q8KV_F32 = 0, Q8KV_F16 = 1, Q8KV_BF16 = 2 } q8kv_dtype;
 /*
  * Decode attention with a library-managed workspace (one per device, grown on demand
  * under a lock, zero-initialised; the first call on a device, or a call that needs a
- * larger workspace, allocates and so must not happen during stream capture). Calls that
- * run concurrently on different streams of one device must use q8kv_decode_attn_ws with
- * separate workspaces.
+ * larger workspace, allocates and so must not happen during stream capture). Smaller ones are
+ * kept, so a captured graph stays valid after such a call. Calls that
+ * run concurrently on different streams of one device, replays of captured graphs among them,
+ * must use q8kv_decode_attn_ws with separate workspaces.
  *
  *   out, q, k_blocks, v_blocks, kscale, vscale, block_table, seq_lens: see the layouts above
  *   B                  batch size (> 0)
@@ -167,6 +168,9 @@ q8kv_status q8kv_decode_attn_multi(float *out, const float *q, const int8_t *k_b
  * layouts and asynchrony as q8kv_decode_attn; kd and vd must be 8-byte aligned. Supported:
  * head_dim 128; group n_q_heads / n_kv_heads <= 16; B * n_kv_heads <= 65535. Two kernel
  * launches (per chunk of 256 tokens, then a merge of the chunks).
+ * The workspace grows with B * max_blocks_per_seq, and a call that needs a larger one frees the
+ * last: a graph captured before such a call must not be replayed after it (make the largest
+ * call first).
  */
 q8kv_status q8kv_decode_attn_q4(float *out, const float *q, const uint8_t *k4_blocks,
                                 const uint8_t *v4_blocks, const uint16_t *kd,
