@@ -254,11 +254,14 @@ __host__ __device__ constexpr int rope_iters(int Hq, int Hk, int D)
 
 constexpr int kRopeTile = 4; // tokens per block and step, at most
 // Resident blocks per SM: a 16-bit row keeps fewer bytes in flight per warp and fewer registers,
-// so there is room and need for a fourth block (13392 bf16 tokens: 78.3 -> 74.1 us).
+// so there is room and need for a fourth block, except where a lane also holds its partners'
+// chunks and would spill at 64 registers (13392 bf16 tokens, 32 / 8 heads of 128, with 3 / 4 blocks:
+// rotary_dim 128 78.3 / 73.8 us, 64 77.7 / 74.2, 128 adjacent 78.6 / 75.8; kRopeAnywhere: 32 101.8
+// / 107.4, 96 106.9 / 112.5; 4999 tokens of 32 40.5 / 44.6).
 template <typename T>
-__host__ __device__ constexpr int rope_blocks()
+__host__ __device__ constexpr int rope_blocks(int mode)
 {
-    return sizeof(T) == 2 ? 4 : 3;
+    return sizeof(T) == 2 && mode != kRopeAnywhere ? 4 : 3;
 }
 
 // A block's share of one step: a tile of tokens, or a part of its iterations.
@@ -268,7 +271,7 @@ struct RopeUnit {
 };
 
 template <int D, typename T, int MODE>
-__global__ void __launch_bounds__(kWriteThreads, rope_blocks<T>())
+__global__ void __launch_bounds__(kWriteThreads, rope_blocks<T>(MODE))
     rope_cache_write_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int LPR = rope_lanes(D);

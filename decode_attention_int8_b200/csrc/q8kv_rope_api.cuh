@@ -39,7 +39,7 @@ q8kv_status launch_rope(RopeParams &p, int mode, int sms, cudaStream_t stream)
     // with a third round for 66 of 1250 tiles). A tile that leaves SMs empty is shared by
     // several blocks, of at least one row group per warp.
     const int iters = rope_iters(p.Hq, p.Hk, D);
-    const long long wave = (long long)rope_blocks<T>() * sms;
+    const long long wave = (long long)rope_blocks<T>(mode) * sms;
     p.tile = 1;
     long long least = 0;
     for (int t = 1; t <= kRopeTile; ++t) {
