@@ -8,8 +8,11 @@
 // the log-sum-exp of each row that the decode left: one pass over K, no softmax to redo.
 //
 // What bounds it: HBM, at 132 bytes of K and 8 of mass per (token, KV head), then the issue
-// slots (48 ragged sequences of up to 16384 tokens, 64 / 8 heads: 73 us, 0.85 of the copy rate;
-// 16 x 4096, 32 / 8: 17 us, 0.67, the rest its start). A warp takes 16 tokens of one head at a
+// slots (48 ragged sequences of up to 16384 tokens, 64 / 8 heads: 73 us in graph replays, 0.85 of
+// the copy rate; 16 x 4096, 32 / 8: 17 us, 0.67, the rest its start; calls from a loop on the host
+// take up to 5 us more of the former). With more than 8 rows per head the operand is read again for
+// every tile and the products and exponentials of the rows bound it (24 x 8192, 32 rows: 71 us,
+// 0.48). A warp takes 16 tokens of one head at a
 // time as the M rows of mma.m16n8k32.s8, query rows as its N columns:
 //  * 5 or more rows per head: eight rows per MMA, one MMA per 32-channel block, K fragments by
 //    ldmatrix.

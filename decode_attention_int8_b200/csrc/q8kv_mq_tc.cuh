@@ -28,8 +28,8 @@
 //    scores, running max A of score + log2 V scale) is kept by lane r of every warp of the
 //    warpgroup, each computing it from the same exchanged maxima, and broadcast with
 //    shuffles.
-//  * PV: the weight w * vs * 2^(M - A + 19) of (token, row) is an exact integer P below
-//    2^23 (A: the largest score + log2 vs, moved only when exceeded by 3); the fp32 bits
+//  * PV: the weight w * vs * 2^(M - A + 22 - h) of (token, row) is an exact integer P below
+//    2^23 (A: the largest score + log2 vs, moved only when exceeded by h); the fp32 bits
 //    of P + 2^23 hold it in their low three bytes. Those 32-bit words are the B operand as
 //    they are: O^T = V^T . W with M = 128 channels (V^T read straight from the swizzled
 //    tile: MN-major int8), N = 4 R columns (row, byte), K = 32 tokens, int32 accumulators in
@@ -672,9 +672,10 @@ __device__ void tc_consume(const DecodeParams &p, uint8_t *smem, const TcLayout 
                     // the reference moves when this tile's largest score + log2 vs exceeds
                     // it by more than the headroom
                     float An = (Arow == -INFINITY || ast > Arow + p.tc_head) ? ast : Arow;
-                    // 2^(M - A + 19) must stay finite: with V scales more than 2^104 below
+                    // 2^(M - A + 22 - h) must stay finite: with V scales more than 2^104 below
                     // the weight of the top-scoring token the reference A is raised to
-                    // M - 104 (the weights of that row then keep fewer significant bits)
+                    // M - 104, at most 2^126 (h = 0) (the weights of that row then keep fewer
+                    // significant bits)
                     if (An != -INFINITY && Mn - An > 104.f)
                         An = Mn - 104.f;
                     cM = Mrow == -INFINITY ? 1.f : fast_exp2(Mrow - Mn);
@@ -688,8 +689,8 @@ __device__ void tc_consume(const DecodeParams &p, uint8_t *smem, const TcLayout 
             }
             const bool fold = __any_sync(kFullMask, rose) || since_fold >= kTcFoldEvery;
 
-            // weights: w = 2^(s - M) into the row sums, P = w vs 2^(M - A + 19) < 2^23 as an
-            // integer in the low mantissa bits of P + 2^23
+            // weights: w = 2^(s - M) into the row sums, P = w vs 2^(M - A + 22 - h) < 2^23 as
+            // an integer in the low mantissa bits of P + 2^23
             uint32_t bits[RH];
 #pragma unroll
             for (int i = 0; i < RH; ++i) {

@@ -21,8 +21,9 @@
 // Neighbouring warps take neighbouring rows, so the block reads and writes contiguous memory.
 // (A first version gave a warp one token and kept its angles in registers: 24 warps per SM at
 // distant addresses, waiting on every token's position -> table chain, ran the 32768-token fp32
-// prompt in 632 us, this one in 229, 0.95 of the copy rate.) Few tokens leave SMs empty, so a
-// tile's rows are then split over several blocks.
+// prompt in 632 us, this one in 229 in graph replays, 0.95 of the copy rate.) Other widths load
+// their rotated chunks twice and spill: 340 us for that prompt at rotary_dim 32 of 128. Few tokens
+// leave SMs empty, so a tile's rows are then split over several blocks.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -11,8 +11,7 @@ using namespace q8kv;
 
 static_assert(kErrPosition == Q8KV_DEVERR_POSITION, "device error bits differ from the header");
 
-// Rotary and verification kernels run on the device of the call's other work: one wave of
-// resident blocks, programmatic dependent launch.
+// A launch of the rotary write or the attention mass: programmatic dependent launch.
 template <typename Params>
 q8kv_status launch_pdl(void (*fn)(Params), const Params &p, unsigned grid, unsigned threads,
                        size_t smem, cudaStream_t stream)

@@ -383,8 +383,8 @@ q8kv_status q8kv_decode_attn_lse(float *out, float *lse, const float *q, const i
  * adds n_queries * n_q_heads / n_kv_heads per KV head (less the rows that see nothing).
  *
  *   mass   fp32 [B][n_kv_heads][max_blocks_per_seq * kv_block_size], updated in place; entries
- *          at or past seq_lens[b] are neither read nor written (a new token's entry starts at
- *          whatever the caller left: zero it, or let q8kv_evict do so)
+ *          at or past seq_lens[b] are not written and have no effect (a new token's entry starts
+ *          at whatever the caller left: zero it, or let q8kv_evict do so)
  *   decay  in [0, 1]: 1 adds up, less forgets, 0 writes the weights without reading mass
  *   lse    fp32 [B][n_queries][n_q_heads]
  * Tokens of a block whose table entry is outside the pool keep their mass
