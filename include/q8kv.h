@@ -390,7 +390,7 @@ q8kv_status q8kv_decode_attn_lse(float *out, float *lse, const float *q, const i
  * Tokens of a block whose table entry is outside the pool keep their mass
  * (Q8KV_DEVERR_BLOCK_TABLE); a seq_len out of range is clamped (Q8KV_DEVERR_SEQ_LEN). A query
  * row that holds an infinity or a NaN, or whose lse is NaN or +inf, gives NaN to every token that
- * it sees, and a scale that is not finite gives its token a mass that is not.
+ * it sees; a scale of NaN, which the cache writes give to such rows, gives NaN to its token.
  * Supported: head_dim 128; kv_block_size a power of two in [16, 256]; n_queries *
  * n_q_heads / n_kv_heads <= 128; n_kv_heads <= 4096; B <= 16384. One kernel launch, no
  * workspace, asynchronous on `stream`, programmatic dependent launch as the other kernels.

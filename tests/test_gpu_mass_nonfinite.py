@@ -46,6 +46,25 @@ def test_a_row_that_is_not_finite(nq, Hq, Hk, what, value):
     assert q8.q8kv_device_errors(clear=True) == 0
 
 
+@pytest.mark.parametrize("nq,Hq,Hk", [(1, 8, 2), (2, 6, 3), (2, 12, 3), (3, 24, 2)])
+def test_a_scale_of_nan(nq, Hq, Hk):
+    """A token whose key row was not finite: NaN for it, and for no other token."""
+    lens = [200, 77]
+    w = inputs.make_custom(2, Hq, Hk, 128, lens, 16, seed=nq + Hq)
+    q = dev(np.asarray(inputs.multi_queries(2, nq, Hq, 128, seed=Hq), np.float32))
+    k, ks, table, seq = (dev(a) for a in (w.k, w.ks, w.block_table, w.seq_lens))
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lse = 2.0 + torch.rand((2, nq, Hq), generator=g, device="cuda")
+    start = torch.rand((2, Hk, w.block_table.shape[1] * 16), generator=g, device="cuda")
+    clean, got = start.clone(), start.clone()
+    q8.q8kv_attn_mass(clean, q, lse, k, ks, table, seq, w.scale)
+    for t in (0, 100, 198, 199):
+        ks[int(w.block_table[0, t // 16]), t % 16, Hk - 1] = NAN
+        clean[0, Hk - 1, t] = NAN
+    q8.q8kv_attn_mass(got, q, lse, k, ks, table, seq, w.scale)
+    assert torch.equal(got.nan_to_num(nan=-1.0), clean.nan_to_num(nan=-1.0))
+
+
 @pytest.mark.parametrize("nq,Hq,Hk", [(1, 8, 2), (1, 32, 2), (2, 16, 4), (4, 32, 4)])
 def test_the_decode_of_such_rows(nq, Hq, Hk):
     """The statistics call: a NaN channel counts as zero (it has no part in its block's maximum and
